@@ -15,14 +15,15 @@
  *   - Host-detectable argument errors are returned synchronously and nothing
  *     is launched.
  *   - Device-detectable errors (a block-table entry outside [0, num_pages), a
- *     candidate count outside [0, k_max], q_len above the declared maximum)
+ *     candidate count outside [0, k_max], q_len above the declared maximum, a
+ *     parent beam outside its group)
  *     are OR-ed into *err_flag (an int32 in device memory, bit (1 << status)),
  *     and the affected work unit is skipped; its outputs are unspecified. The
  *     caller clears the flag and reads it when it chooses. err_flag may be
  *     NULL, in which case such errors are dropped silently.
  *   - Workspaces are caller-owned device buffers of at least the size the
- *     matching *_workspace_size call returns, 256-byte aligned. Both the
- *     sa_paged_attn and the sa_spec_verify_greedy workspace must be
+ *     matching *_workspace_size call returns, 256-byte aligned. The
+ *     sa_paged_attn, sa_spec_verify_greedy and sa_beam_select workspaces must be
  *     ZERO-FILLED BEFORE THEIR FIRST USE (they hold counters), and every call
  *     that completes without a device error leaves those counters at zero
  *     again; after a call that set a device error flag, zero the workspace
@@ -48,7 +49,7 @@ extern "C" {
 
 typedef enum {
     SA_OK = 0,
-    SA_ERR_ARG = 1,          /* bad pointer, size or shape (host check) */
+    SA_ERR_ARG = 1,          /* bad pointer, size or shape (host check), parent beam out of range (device flag) */
     SA_ERR_UNSUPPORTED = 2,  /* valid but not implemented (e.g. head_dim != 128) */
     SA_ERR_PAGE_OOB = 3,     /* block-table entry outside [0, num_pages) (device flag) */
     SA_ERR_CUDA = 4,         /* a CUDA runtime call failed */
@@ -409,6 +410,176 @@ SA_API int sa_defrag_apply(const sa_dims *dims, uint16_t *k_pages, uint16_t *v_p
  */
 SA_API int sa_defrag_apply_bytes(int32_t num_pages, int64_t page_bytes, void *pool_a, void *pool_b,
                                  const int32_t *moves, int32_t n_moves, int32_t *err_flag, void *stream);
+
+/* Norm and position rotation of query and key heads: sa_qk_norm_rope and the
+ * sa_kv_append_rope calls. The struct is host memory, its arrays device memory.
+ *
+ * A head x of 128 values with a weight w becomes y = x * rsqrt(mean(x^2) + eps)
+ * * w; with no weight y = x. Then, with R = rotary_dim and
+ * t = position * inv_freq[j] for j < R / 2, the pair (a, b) of
+ *   y[j], y[j + R/2]       (interleaved 0)
+ *   y[2j], y[2j + 1]       (interleaved non-zero)
+ * becomes (a cos t - b sin t, a sin t + b cos t); y[R ..] stay. Held in fp32
+ * throughout (t in 64 bits, for any int32 position) and rounded once. */
+typedef struct {
+    const float *inv_freq; /* device fp32 [rotary_dim / 2] */
+    const float *q_weight; /* device fp32 [128], 16-byte aligned, or NULL: queries have no norm */
+    const float *k_weight; /* the same for keys */
+    float eps;             /* in (0, 1]; read when there is a weight */
+    int32_t rotary_dim;    /* R: 0 (no rotation) or a multiple of 16 up to 128 */
+    int32_t interleaved;
+} sa_rope;
+
+/*
+ * sa_qk_norm_rope -- norm and rotation of queries and keys in one pass.
+ *
+ *   q, q_out     device bf16 [num_tokens, num_q_heads, 128]: a token's heads
+ *                are packed, *_stride is the distance between tokens in values
+ *                (a multiple of 8, at least heads * 128), so the views of one
+ *                projection's output can be passed as they are. 16-byte
+ *                aligned. num_q_heads 0: no queries (q, q_out NULL).
+ *   k, k_out     the same with num_kv_heads
+ *   positions    device int32 [num_tokens], any values
+ * An output may be its own input (same pointer and stride); otherwise the
+ * outputs overlap neither inputs nor each other. head_dim must be 128.
+ */
+SA_API int sa_qk_norm_rope(const sa_rope *rope, int32_t num_tokens, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, const uint16_t *q, int64_t q_stride,
+                           const uint16_t *k, int64_t k_stride, const int32_t *positions,
+                           uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out,
+                           int64_t k_out_stride, void *stream);
+
+/*
+ * sa_kv_append_rope -- sa_kv_append with norm and rotation on the way, and the
+ * queries in the same launch.
+ *
+ * ExLlamaV2 "Dynamic Generator" page, section "Continuous batching", as in
+ * sa_kv_append. The key rows are normalised and rotated (sa_rope) before they
+ * are written to their page, the value rows are written as they are, and
+ * q_out[row] receives the normalised and rotated queries, ready for
+ * sa_paged_attn. The position of new token i of sequence b is
+ * seq_lens[b] - q_lens[b] + i, or positions[row] where positions is given (the
+ * page and slot are those of the cache position either way).
+ *   q            device bf16 [total_q, num_q_heads, 128], or NULL with q_out NULL
+ *   k_new, v_new device bf16 [total_q, num_kv_heads, 128]
+ *                strides and alignment as in sa_qk_norm_rope
+ *   q_out        device bf16 [total_q, num_q_heads, 128], packed; may be q
+ *   positions    device int32 [total_q] or NULL
+ *   others       as in sa_kv_append (bf16 pages 16-byte aligned)
+ * Rows of q_out behind the last sequence's are not written. A sequence whose
+ * q_lens or seq_lens are inconsistent sets SA_ERR_QLEN and is skipped; a page id
+ * out of range sets SA_ERR_PAGE_OOB and the page rows are skipped.
+ * Like sa_kv_append the kernel lets a following sa_paged_attn start early.
+ *
+ * sa_kv_append_rope_q8, sa_kv_append_rope_q4: the same into int8 and int4 pages
+ * (formats of sa_kv_append_q8 and _q4, 16-byte aligned codes); keys are
+ * quantised from their fp32 values.
+ */
+SA_API int sa_kv_append_rope(const sa_dims *dims, const sa_rope *rope, const uint16_t *q, int64_t q_stride,
+                             const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
+                             int64_t v_stride, uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages,
+                             const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                             const int32_t *positions, int32_t *err_flag, void *stream);
+SA_API int sa_kv_append_rope_q8(const sa_dims *dims, const sa_rope *rope, const uint16_t *q,
+                                int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                                const uint16_t *v_new, int64_t v_stride, uint16_t *q_out, int8_t *k_codes,
+                                int8_t *v_codes, float *k_scales, float *v_scales,
+                                const int32_t *block_table, const int32_t *seq_lens,
+                                const int32_t *q_lens, const int32_t *positions, int32_t *err_flag,
+                                void *stream);
+SA_API int sa_kv_append_rope_q4(const sa_dims *dims, const sa_rope *rope, const uint16_t *q,
+                                int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                                const uint16_t *v_new, int64_t v_stride, uint16_t *q_out, uint8_t *k_codes,
+                                uint8_t *v_codes, float *k_scales, float *v_scales,
+                                const int32_t *block_table, const int32_t *seq_lens,
+                                const int32_t *q_lens, const int32_t *positions, int32_t *err_flag,
+                                void *stream);
+
+/* Bytes of workspace sa_beam_select needs (0 for shapes it refuses). */
+SA_API size_t sa_beam_select_workspace_size(int32_t num_groups, int32_t beam_width, int32_t vocab,
+                                            int32_t num_select);
+
+/*
+ * sa_beam_select -- the best continuations of each group's beams.
+ *
+ * Beam search (not on the pages, which answer greedily): the continuation of
+ * beam w by token t has the value
+ *   scores[w] + (x[t] - log(sum_u exp(x[u]))),  x = logits of beam w;
+ * a finished beam has one continuation, eos_token at the value scores[w], all
+ * its others have the value -inf. The num_select largest of a group's
+ * beam_width * vocab values are written, largest first. Equal values: the lower
+ * beam first, inside a beam the larger logit, then the lower token (of a
+ * finished beam eos_token, then the lower token). A NaN logit counts as -inf,
+ * +inf as the largest finite value, a NaN score as -inf.
+ *   logits       device fp32 (sa_beam_select) or bf16 (_bf16), one row of vocab
+ *                values a beam, [num_groups * beam_width] rows logits_stride
+ *                values apart (>= vocab); any alignment of whole values
+ *   scores       device fp32 [num_groups, beam_width], sums of log-probabilities
+ *                (-inf: a beam not in use, as all but the first before the first step)
+ *   finished     device int32 [num_groups, beam_width], non-zero: finished; or NULL
+ *   eos_token    the end token, or -1 (with finished and finished_out NULL)
+ *   tokens, parents  device int32 [num_groups, num_select] (outputs): token and
+ *                beam inside the group
+ *   scores_out   device fp32 [num_groups, num_select] (output)
+ *   finished_out device int32 [num_groups, num_select] (output) or NULL: 1 where
+ *                the parent was finished or the token is eos_token, else 0
+ *   workspace    device, >= sa_beam_select_workspace_size(...) bytes
+ * scores_out and finished_out may be scores and finished (num_select =
+ * beam_width). beam_width and num_select at most 32, num_groups at most 16384,
+ * vocab at most 2^26, else SA_ERR_UNSUPPORTED. A row's sum is accurate to about
+ * 1e-7, the values and the comparisons of beams are in 64 bits. One kernel, the
+ * same results on every call.
+ */
+SA_API int sa_beam_select(const float *logits, int64_t logits_stride, const float *scores,
+                          const int32_t *finished, int32_t num_groups, int32_t beam_width, int32_t vocab,
+                          int32_t num_select, int32_t eos_token, int32_t *tokens, int32_t *parents,
+                          float *scores_out, int32_t *finished_out, void *workspace,
+                          size_t workspace_bytes, void *stream);
+SA_API int sa_beam_select_bf16(const uint16_t *logits, int64_t logits_stride, const float *scores,
+                               const int32_t *finished, int32_t num_groups, int32_t beam_width,
+                               int32_t vocab, int32_t num_select, int32_t eos_token, int32_t *tokens,
+                               int32_t *parents, float *scores_out, int32_t *finished_out, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * sa_beam_reorder -- the cache behind the chosen continuations.
+ *
+ * Sequences b = group * beam_width + i are a group's beams; all beams of a group
+ * have the same length T = seq_lens[b]. Pages before T / 256 are full and may be
+ * shared by the beams (ExLlamaV2 "Dynamic Generator" page, section
+ * "Deduplication"); a table's entries from T / 256 on are pages of that beam
+ * alone (or unset), also those that the caller reserves ahead for tokens to come.
+ * New beam i continues old beam p = parents[b]:
+ *   - its table row starts with p's entries before T / 256;
+ *   - the lowest i of a parent takes the parent's entries from T / 256 on; the
+ *     k-th other beam of the group (by increasing i) takes those of the k-th beam
+ *     that no new beam continues, and the T % 256 rows of p's page T / 256 are
+ *     copied into its own.
+ * Full pages that no table names any more are the caller's to reuse.
+ *   parents      device int32 [num_seqs], each in [0, beam_width) (the parents of
+ *                sa_beam_select with num_select = beam_width)
+ *   block_table  device int32 [num_seqs, max_pages_per_seq], read
+ *   seq_lens     device int32 [num_seqs]; lengths do not change
+ *   block_table_out  device int32, same shape, not overlapping block_table
+ *   k_pages, v_pages  as in sa_kv_append (16-byte aligned), written in place
+ * Uses num_seqs, num_kv_heads, num_pages and max_pages_per_seq of dims;
+ * beam_width at most 32. A group with a parent out of range (SA_ERR_ARG) or
+ * lengths that differ or do not fit the table (SA_ERR_QLEN) is skipped, and so is the
+ * copy of a page out of range (SA_ERR_PAGE_OOB).
+ *
+ * sa_beam_reorder_q8, sa_beam_reorder_q4: the same over int8 and int4 pages.
+ */
+SA_API int sa_beam_reorder(const sa_dims *dims, int32_t beam_width, const int32_t *parents,
+                           const int32_t *block_table, const int32_t *seq_lens, int32_t *block_table_out,
+                           uint16_t *k_pages, uint16_t *v_pages, int32_t *err_flag, void *stream);
+SA_API int sa_beam_reorder_q8(const sa_dims *dims, int32_t beam_width, const int32_t *parents,
+                              const int32_t *block_table, const int32_t *seq_lens, int32_t *block_table_out,
+                              int8_t *k_codes, int8_t *v_codes, float *k_scales, float *v_scales,
+                              int32_t *err_flag, void *stream);
+SA_API int sa_beam_reorder_q4(const sa_dims *dims, int32_t beam_width, const int32_t *parents,
+                              const int32_t *block_table, const int32_t *seq_lens, int32_t *block_table_out,
+                              uint8_t *k_codes, uint8_t *v_codes, float *k_scales, float *v_scales,
+                              int32_t *err_flag, void *stream);
 
 #ifdef __cplusplus
 }

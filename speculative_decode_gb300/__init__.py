@@ -9,8 +9,14 @@ not build anything (``speculative_decode_gb300.build.build()`` does).
 from ._lib import (  # noqa: F401
     Dims,
     Plan,
+    Rope,
     SpecAttnError,
     STATUS,
+    beam_reorder,
+    beam_reorder_q4,
+    beam_reorder_q8,
+    beam_select,
+    beam_select_workspace_size,
     defrag_apply,
     defrag_apply_bytes,
     defrag_moves,
@@ -18,6 +24,9 @@ from ._lib import (  # noqa: F401
     kv_append,
     kv_append_q4,
     kv_append_q8,
+    kv_append_rope,
+    kv_append_rope_q4,
+    kv_append_rope_q8,
     library_path,
     load_library,
     paged_attn,
@@ -27,6 +36,7 @@ from ._lib import (  # noqa: F401
     paged_attn_noalloc,
     paged_attn_workspace_size,
     plan_analyze,
+    qk_norm_rope,
     selftest_bounded_wait,
     sm_count,
     spec_verify_greedy,

@@ -31,6 +31,11 @@ class Dims(ctypes.Structure):
         "max_pages_per_seq", "total_q", "max_q_len")]
 
 
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -50,7 +55,8 @@ def load_library() -> ctypes.CDLL:
                            "(or __graft_entry__.build()); there is no fallback path")
     lib = ctypes.CDLL(path)
     P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-    DP = ctypes.POINTER(Dims)
+    I64 = ctypes.c_int64
+    DP, RP = ctypes.POINTER(Dims), ctypes.POINTER(_RopeStruct)
     sig = {
         "sa_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "sa_device_sm_count": ([], ctypes.c_int),
@@ -74,6 +80,16 @@ def load_library() -> ctypes.CDLL:
         "sa_defrag_moves": ([DP, P, P, P, P, P, P], ctypes.c_int),
         "sa_defrag_apply": ([DP, P, P, P, I32, P, P], ctypes.c_int),
         "sa_defrag_apply_bytes": ([I32, ctypes.c_int64, P, P, P, I32, P, P], ctypes.c_int),
+        "sa_qk_norm_rope": ([RP, I32, I32, I32, I32, P, I64, P, I64, P, P, I64, P, I64, P], ctypes.c_int),
+        "sa_kv_append_rope": ([DP, RP, P, I64, P, I64, P, I64] + [P] * 9, ctypes.c_int),
+        "sa_kv_append_rope_q8": ([DP, RP, P, I64, P, I64, P, I64] + [P] * 11, ctypes.c_int),
+        "sa_kv_append_rope_q4": ([DP, RP, P, I64, P, I64, P, I64] + [P] * 11, ctypes.c_int),
+        "sa_beam_select_workspace_size": ([I32, I32, I32, I32], SZ),
+        "sa_beam_select": ([P, I64, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P], ctypes.c_int),
+        "sa_beam_select_bf16": ([P, I64, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P], ctypes.c_int),
+        "sa_beam_reorder": ([DP, I32] + [P] * 8, ctypes.c_int),
+        "sa_beam_reorder_q8": ([DP, I32] + [P] * 10, ctypes.c_int),
+        "sa_beam_reorder_q4": ([DP, I32] + [P] * 10, ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -315,3 +331,235 @@ def defrag_apply_bytes(num_pages: int, page_bytes: int, pool_a, pool_b, moves, n
     rc = load_library().sa_defrag_apply_bytes(int(num_pages), int(page_bytes), _ptr(pool_a), _ptr(pool_b),
                                               _ptr(moves), int(n_moves), _ptr(err_flag), _stream(stream))
     _check(rc, "sa_defrag_apply_bytes")
+
+
+class _Types:
+    """torch dtypes by what the C ABI calls them (torch is imported with the first call that needs it)."""
+
+    def __init__(self):
+        import torch
+        self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)  # values or bit patterns
+        self.f32 = (torch.float32,)
+        self.i32 = (torch.int32,)
+        self.i8 = (torch.int8,)
+        self.u8 = (torch.uint8,)
+        self.current_device = torch.cuda.current_device
+
+
+_types_made = None
+
+
+def _types() -> _Types:
+    global _types_made
+    if _types_made is None:
+        _types_made = _Types()
+    return _types_made
+
+
+def _tensor(t, name: str, dtypes, shape=None, optional=False):
+    """Address of a packed CUDA tensor of one of these dtypes (and of that shape)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtypes[0]} is wanted, got {t.dtype}, strides "
+                         f"{t.stride()}, on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, name: str, tokens: int, heads: int):
+    """(address, token stride) of bf16 rows [tokens, heads, 128] whose heads are packed in their token."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda or t.dtype not in _types().bf16:
+        raise ValueError(f"{name}: a CUDA tensor of bf16 values is wanted, got {t.dtype} on {t.device}")
+    if t.shape != (tokens, heads, 128):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {(tokens, heads, 128)}")
+    step, head, value = t.stride()
+    if tokens and (value != 1 or (head != 128 and heads > 1)):
+        raise ValueError(f"{name}: a token's heads and their values must be packed, strides {t.stride()}")
+    return t.data_ptr(), (step if tokens > 1 else heads * 128)
+
+
+def _same_device(*tensors) -> None:
+    """The tensors of a call are on the device that is current: its context takes the launch."""
+    here = _types().current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
+class Rope:
+    """Norm and rotation of query and key heads (sa_rope): frequencies fp32
+    [rotary_dim / 2], weights fp32 [128] or None for no norm. Made once for a
+    model's layer; it keeps its tensors."""
+
+    def __init__(self, inv_freq=None, rotary_dim=128, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
+        f32 = _types().f32
+        self._struct = _RopeStruct(
+            _tensor(inv_freq, "inv_freq", f32, (rotary_dim // 2,), optional=rotary_dim == 0),
+            _tensor(q_weight, "q_weight", f32, (128,), optional=True),
+            _tensor(k_weight, "k_weight", f32, (128,), optional=True),
+            eps, rotary_dim, 1 if interleaved else 0)
+        self._kept = (inv_freq, q_weight, k_weight)
+        _same_device(*self._kept)
+        self._ref = ctypes.byref(self._struct)
+
+
+def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None:
+    """sa_qk_norm_rope: q [tokens, heads, 128] -> q_out and k -> k_out, normalised
+    and rotated. q and k may be views with any token stride (a multiple of 8
+    values); q with q_out, or k with k_out, may be None."""
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise ValueError("q with q_out, k with k_out, or both are wanted")
+    n = (k if q is None else q).shape[0]
+    hq = 0 if q is None else q.shape[1]
+    hk = 0 if k is None else k.shape[1]
+    qp, qs = (None, 0) if q is None else _heads(q, "q", n, hq)
+    qo, qos = (None, 0) if q is None else _heads(q_out, "q_out", n, hq)
+    kp, ks = (None, 0) if k is None else _heads(k, "k", n, hk)
+    ko, kos = (None, 0) if k is None else _heads(k_out, "k_out", n, hk)
+    pos = _tensor(positions, "positions", _types().i32, (n,))
+    _same_device(q, k, positions, q_out, k_out, *rope._kept)
+    _check(load_library().sa_qk_norm_rope(rope._ref, n, hq, hk, 128, qp, qs, kp, ks, pos, qo, qos, ko, kos,
+                                          _stream(stream)), "sa_qk_norm_rope")
+
+
+def _append_rope(name, dims, rope, q, k_new, v_new, q_out, pools, pool_types, block_table, seq_lens, q_lens,
+                 positions, err_flag, stream) -> None:
+    n, hkv, pages, B = dims.total_q, dims.num_kv_heads, dims.num_pages, dims.num_seqs
+    types = _types()
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    qp, qs, qo = None, 0, None
+    if q is not None:
+        qp, qs = _heads(q, "q", n, dims.num_q_heads)
+        qo = _tensor(q_out, "q_out", types.bf16, (n, dims.num_q_heads, 128))
+    kp, ks = _heads(k_new, "k_new", n, hkv)
+    vp, vs = _heads(v_new, "v_new", n, hkv)
+    addresses = [_tensor(t, "page pool", dt, (pages, hkv, 256, row) if row else (pages, hkv, 256))
+                 for t, (dt, row) in zip(pools, pool_types)]
+    bt = _tensor(block_table, "block_table", types.i32, (B, dims.max_pages_per_seq))
+    sl = _tensor(seq_lens, "seq_lens", types.i32, (B,))
+    ql = _tensor(q_lens, "q_lens", types.i32, (B,))
+    ps = _tensor(positions, "positions", types.i32, (n,), optional=True)
+    err = _tensor(err_flag, "err_flag", types.i32, optional=True)
+    _same_device(q, q_out, k_new, v_new, *pools, block_table, seq_lens, q_lens, positions, err_flag, *rope._kept)
+    _check(getattr(load_library(), name)(ctypes.byref(dims), rope._ref, qp, qs, kp, ks, vp, vs, qo, *addresses, bt, sl,
+                                         ql, ps, err, _stream(stream)), name)
+
+
+def kv_append_rope(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, q_lens,
+                   positions=None, err_flag=None, stream=None) -> None:
+    """sa_kv_append_rope: kv_append with the keys normalised and rotated on the
+    way, and q -> q_out for paged_attn (q and q_out may be None). q, k_new and
+    v_new may be views with any token stride (a multiple of 8 values)."""
+    bf16 = _types().bf16
+    _append_rope("sa_kv_append_rope", dims, rope, q, k_new, v_new, q_out, (k_pages, v_pages), ((bf16, 128),) * 2,
+                 block_table, seq_lens, q_lens, positions, err_flag, stream)
+
+
+def kv_append_rope_q8(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_codes, v_codes, k_scales, v_scales,
+                      block_table, seq_lens, q_lens, positions=None, err_flag=None, stream=None) -> None:
+    """kv_append_rope into int8 pages (pools as in kv_append_q8)."""
+    t = _types()
+    _append_rope("sa_kv_append_rope_q8", dims, rope, q, k_new, v_new, q_out, (k_codes, v_codes, k_scales, v_scales),
+                 ((t.i8, 128), (t.i8, 128), (t.f32, 0), (t.f32, 0)), block_table, seq_lens, q_lens, positions, err_flag,
+                 stream)
+
+
+def kv_append_rope_q4(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_codes, v_codes, k_scales, v_scales,
+                      block_table, seq_lens, q_lens, positions=None, err_flag=None, stream=None) -> None:
+    """kv_append_rope into int4 pages (pools as in kv_append_q4)."""
+    t = _types()
+    _append_rope("sa_kv_append_rope_q4", dims, rope, q, k_new, v_new, q_out, (k_codes, v_codes, k_scales, v_scales),
+                 ((t.u8, 64), (t.u8, 64), (t.f32, 0), (t.f32, 0)), block_table, seq_lens, q_lens, positions, err_flag,
+                 stream)
+
+
+def beam_select_workspace_size(num_groups: int, beam_width: int, vocab: int, num_select: int) -> int:
+    return int(load_library().sa_beam_select_workspace_size(num_groups, beam_width, vocab, num_select))
+
+
+def beam_select(logits, scores, tokens, parents, scores_out, workspace, finished=None, finished_out=None,
+                eos_token: int = -1, stream=None) -> None:
+    """sa_beam_select (fp32 logits) or sa_beam_select_bf16 (bf16 logits): the best
+    continuations of every group. logits [groups, beams, vocab] may be a view
+    whose rows are evenly spaced (a padded vocabulary); scores and finished
+    [groups, beams]; the outputs [groups, picks]."""
+    types = _types()
+    wide = logits.dtype in types.f32
+    if logits.dim() != 3 or not logits.is_cuda or not (wide or logits.dtype in types.bf16):
+        raise ValueError(f"logits: fp32 or bf16 values [groups, beams, vocab] on a GPU are wanted, got {logits.dtype} "
+                         f"{tuple(logits.shape)} on {logits.device}")
+    B, W, V = logits.shape
+    group, row, value = logits.stride()
+    if W == 1:
+        row = group if B > 1 else V
+    if (V > 1 and value != 1) or (B > 1 and group != W * row):
+        raise ValueError(f"logits: packed values and evenly spaced rows are wanted, strides {logits.stride()}")
+    if B * W <= 1:
+        row = V
+    K = tokens.shape[-1]
+    picks, beams = (B, K), (B, W)
+    sc = _tensor(scores, "scores", types.f32, beams)
+    fi = _tensor(finished, "finished", types.i32, beams, optional=True)
+    to = _tensor(tokens, "tokens", types.i32, picks)
+    pa = _tensor(parents, "parents", types.i32, picks)
+    so = _tensor(scores_out, "scores_out", types.f32, picks)
+    fo = _tensor(finished_out, "finished_out", types.i32, picks, optional=True)
+    ws = _tensor(workspace, "workspace", types.u8)
+    _same_device(logits, scores, tokens, parents, scores_out, workspace, finished, finished_out)
+    lib = load_library()
+    call = lib.sa_beam_select if wide else lib.sa_beam_select_bf16
+    _check(call(logits.data_ptr(), row, sc, fi, B, W, V, K, eos_token, to, pa, so, fo, ws, workspace.numel(),
+                _stream(stream)), "sa_beam_select")
+
+
+def _beam_reorder(name, dims, beam_width, parents, block_table, seq_lens, block_table_out, pools, pool_types, err_flag,
+                  stream) -> None:
+    types = _types()
+    B, hkv, pages = dims.num_seqs, dims.num_kv_heads, dims.num_pages
+    table = (B, dims.max_pages_per_seq)
+    addresses = [_tensor(t, "page pool", dt, (pages, hkv, 256, row) if row else (pages, hkv, 256))
+                 for t, (dt, row) in zip(pools, pool_types)]
+    pa = _tensor(parents, "parents", types.i32)
+    if parents.numel() != B:
+        raise ValueError(f"parents: {parents.numel()} values for {B} sequences")
+    bt = _tensor(block_table, "block_table", types.i32, table)
+    sl = _tensor(seq_lens, "seq_lens", types.i32, (B,))
+    bo = _tensor(block_table_out, "block_table_out", types.i32, table)
+    err = _tensor(err_flag, "err_flag", types.i32, optional=True)
+    _same_device(parents, block_table, seq_lens, block_table_out, *pools, err_flag)
+    _check(getattr(load_library(), name)(ctypes.byref(dims), beam_width, pa, bt, sl, bo, *addresses, err,
+                                         _stream(stream)), name)
+
+
+def beam_reorder(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_pages, v_pages,
+                 err_flag=None, stream=None) -> None:
+    """sa_beam_reorder: the tables of the chosen continuations, and the copies of
+    the tail pages that more than one of them continues."""
+    bf16 = _types().bf16
+    _beam_reorder("sa_beam_reorder", dims, beam_width, parents, block_table, seq_lens, block_table_out,
+                  (k_pages, v_pages), ((bf16, 128),) * 2, err_flag, stream)
+
+
+def beam_reorder_q8(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_codes, v_codes,
+                    k_scales, v_scales, err_flag=None, stream=None) -> None:
+    """beam_reorder over int8 pages."""
+    t = _types()
+    _beam_reorder("sa_beam_reorder_q8", dims, beam_width, parents, block_table, seq_lens, block_table_out,
+                  (k_codes, v_codes, k_scales, v_scales), ((t.i8, 128), (t.i8, 128), (t.f32, 0), (t.f32, 0)), err_flag,
+                  stream)
+
+
+def beam_reorder_q4(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_codes, v_codes,
+                    k_scales, v_scales, err_flag=None, stream=None) -> None:
+    """beam_reorder over int4 pages."""
+    t = _types()
+    _beam_reorder("sa_beam_reorder_q4", dims, beam_width, parents, block_table, seq_lens, block_table_out,
+                  (k_codes, v_codes, k_scales, v_scales), ((t.u8, 64), (t.u8, 64), (t.f32, 0), (t.f32, 0)), err_flag,
+                  stream)

@@ -670,6 +670,330 @@ int sa_defrag_apply_bytes(int32_t num_pages, int64_t page_bytes, void *pool_a, v
 }
 
 // ---------------------------------------------------------------------------
+// Norm and rotation of queries and keys, and the append that makes it on the
+// way.
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_rope(const sa_rope *r, int head_dim) {
+    if (r == nullptr) return SA_ERR_ARG;
+    if (head_dim != kHeadDim) return SA_ERR_UNSUPPORTED;
+    if (r->rotary_dim < 0 || r->rotary_dim > kHeadDim || r->rotary_dim % 2 != 0) return SA_ERR_ARG;
+    if (r->rotary_dim % 16 != 0) return SA_ERR_UNSUPPORTED;
+    if (r->rotary_dim > 0 && r->inv_freq == nullptr) return SA_ERR_ARG;
+    if ((r->q_weight != nullptr || r->k_weight != nullptr) && !(r->eps > 0.f && r->eps <= 1.f)) return SA_ERR_ARG;
+    if (!aligned(r->inv_freq, 4) || !aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return SA_ERR_ARG;
+    return SA_OK;
+}
+
+// A tensor of `heads` packed heads a token (heads 0: absent).
+bool rows_ok(const void *p, int64_t stride, int64_t heads) {
+    if (heads == 0) return true;
+    return p != nullptr && aligned(p, 16) && stride >= heads * kHeadDim && stride % 8 == 0;
+}
+
+void set_rope(RopeParams &p, const sa_rope &r) {
+    p.inv_freq = r.inv_freq;
+    p.q_weight = r.q_weight;
+    p.k_weight = r.k_weight;
+    p.eps = r.eps;
+    p.half = r.rotary_dim / 2;
+    p.interleaved = r.interleaved != 0;
+}
+
+}  // namespace
+
+int sa_qk_norm_rope(const sa_rope *rope, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                    int32_t head_dim, const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                    const int32_t *positions, uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out,
+                    int64_t k_out_stride, void *stream) {
+    int rc = check_rope(rope, head_dim);
+    if (rc) return rc;
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0) return SA_ERR_ARG;
+    if (num_q_heads > kMaxRopeHeads || num_kv_heads > kMaxRopeHeads) return SA_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return SA_OK;
+    if (positions == nullptr || !aligned(positions, 4)) return SA_ERR_ARG;
+    if (!rows_ok(q, q_stride, num_q_heads) || !rows_ok(q_out, q_out_stride, num_q_heads) ||
+        !rows_ok(k, k_stride, num_kv_heads) || !rows_ok(k_out, k_out_stride, num_kv_heads))
+        return SA_ERR_ARG;
+    RopeParams p{};
+    set_rope(p, *rope);
+    p.q = q;
+    p.k = k;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.positions = positions;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_rope(p, 0, num_tokens, s) != cudaSuccess) return SA_ERR_CUDA;
+    return finish(s, nullptr);
+}
+
+static int append_rope(const sa_dims *dims, const sa_rope *rope, RopeParams &p, int bits, void *stream) {
+    int rc = check_dims(dims);
+    if (rc) return rc;
+    const sa_dims &d = *dims;
+    rc = check_rope(rope, d.head_dim);
+    if (rc) return rc;
+    if (d.num_q_heads > kMaxRopeHeads) return SA_ERR_UNSUPPORTED;
+    if ((p.q == nullptr) != (p.q_out == nullptr)) return SA_ERR_ARG;
+    if (d.num_seqs == 0 || d.total_q == 0) return SA_OK;
+    const int64_t hq = p.q == nullptr ? 0 : d.num_q_heads;
+    if (!rows_ok(p.q, p.q_stride, hq) || !rows_ok(p.k, p.k_stride, d.num_kv_heads) ||
+        !rows_ok(p.v, p.v_stride, d.num_kv_heads) || !aligned(p.q_out, 16))
+        return SA_ERR_ARG;
+    if (bits == 16 ? (!p.k_pages || !p.v_pages || !aligned(p.k_pages, 16) || !aligned(p.v_pages, 16))
+                   : (!p.k_codes || !p.v_codes || !p.k_scales || !p.v_scales || !aligned(p.k_codes, 16) ||
+                      !aligned(p.v_codes, 16) || !aligned(p.k_scales, 4) || !aligned(p.v_scales, 4)))
+        return SA_ERR_ARG;
+    if (!p.block_table || !p.seq_lens || !p.q_lens) return SA_ERR_ARG;
+    set_rope(p, *rope);
+    p.q_out_stride = hq * kHeadDim;
+    p.B = d.num_seqs;
+    p.Hq = static_cast<int32_t>(hq);
+    p.Hkv = d.num_kv_heads;
+    p.num_pages = d.num_pages;
+    p.max_pages = d.max_pages_per_seq;
+    p.max_q_len = d.max_q_len;
+    p.total_q = d.total_q;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_rope(p, bits, d.total_q, s) != cudaSuccess) return SA_ERR_CUDA;
+    return finish(s, p.err);
+}
+
+// The arguments that the three appends share.
+static RopeParams append_rope_params(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                                     const uint16_t *v_new, int64_t v_stride, uint16_t *q_out,
+                                     const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                                     const int32_t *positions, int32_t *err_flag) {
+    RopeParams p{};
+    p.q = q;
+    p.q_stride = q_stride;
+    p.k = k_new;
+    p.k_stride = k_stride;
+    p.v = v_new;
+    p.v_stride = v_stride;
+    p.q_out = q_out;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.q_lens = q_lens;
+    p.positions = positions;
+    p.err = err_flag;
+    return p;
+}
+
+int sa_kv_append_rope(const sa_dims *dims, const sa_rope *rope, const uint16_t *q, int64_t q_stride,
+                      const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new, int64_t v_stride,
+                      uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *q_lens, const int32_t *positions, int32_t *err_flag,
+                      void *stream) {
+    RopeParams p = append_rope_params(q, q_stride, k_new, k_stride, v_new, v_stride, q_out, block_table, seq_lens,
+                                      q_lens, positions, err_flag);
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    return append_rope(dims, rope, p, 16, stream);
+}
+
+int sa_kv_append_rope_q8(const sa_dims *dims, const sa_rope *rope, const uint16_t *q, int64_t q_stride,
+                         const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new, int64_t v_stride,
+                         uint16_t *q_out, int8_t *k_codes, int8_t *v_codes, float *k_scales, float *v_scales,
+                         const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                         const int32_t *positions, int32_t *err_flag, void *stream) {
+    RopeParams p = append_rope_params(q, q_stride, k_new, k_stride, v_new, v_stride, q_out, block_table, seq_lens,
+                                      q_lens, positions, err_flag);
+    p.k_codes = reinterpret_cast<uint8_t *>(k_codes);
+    p.v_codes = reinterpret_cast<uint8_t *>(v_codes);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    return append_rope(dims, rope, p, 8, stream);
+}
+
+int sa_kv_append_rope_q4(const sa_dims *dims, const sa_rope *rope, const uint16_t *q, int64_t q_stride,
+                         const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new, int64_t v_stride,
+                         uint16_t *q_out, uint8_t *k_codes, uint8_t *v_codes, float *k_scales, float *v_scales,
+                         const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                         const int32_t *positions, int32_t *err_flag, void *stream) {
+    RopeParams p = append_rope_params(q, q_stride, k_new, k_stride, v_new, v_stride, q_out, block_table, seq_lens,
+                                      q_lens, positions, err_flag);
+    p.k_codes = k_codes;
+    p.v_codes = v_codes;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    return append_rope(dims, rope, p, 4, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Beam search: selection and reordering.
+// ---------------------------------------------------------------------------
+namespace {
+
+// Workspace: one counter a group (zero between calls) in a region of fixed
+// size, so that one workspace serves calls of any shape; then the chunks'
+// picks and their sums, for the finest cut of the rows.
+constexpr int kSelectMaxGroups = 16384;
+constexpr size_t kSelectCounterBytes = kSelectMaxGroups * 4;
+
+struct SelectLayout {
+    size_t keys_offset, sums_offset, total;
+};
+
+int64_t select_chunks(int64_t vocab, int values) { return (vocab + values - 1) / values; }
+
+SelectLayout select_layout(int64_t groups, int64_t width, int64_t vocab, int64_t picks) {
+    const int64_t lists = groups * width * select_chunks(vocab, beam_select_chunk_values(false));
+    SelectLayout w{};
+    w.keys_offset = kSelectCounterBytes;
+    w.sums_offset = w.keys_offset + align256(static_cast<size_t>(lists * picks * 8));
+    w.total = w.sums_offset + align256(static_cast<size_t>(lists * 8));
+    return w;
+}
+
+int check_select(int32_t groups, int32_t width, int32_t vocab, int32_t picks) {
+    if (groups < 0 || width <= 0 || vocab <= 0 || picks <= 0) return SA_ERR_ARG;
+    if (static_cast<int64_t>(picks) > static_cast<int64_t>(width) * vocab) return SA_ERR_ARG;
+    if (width > kMaxBeamWidth || picks > kMaxBeamWidth || vocab > (1 << 26)) return SA_ERR_UNSUPPORTED;
+    if (groups > kSelectMaxGroups) return SA_ERR_UNSUPPORTED;
+    // the finest cut's CTAs fit a grid
+    if (static_cast<int64_t>(groups) * width * select_chunks(vocab, beam_select_chunk_values(false)) > INT32_MAX)
+        return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+}  // namespace
+
+size_t sa_beam_select_workspace_size(int32_t num_groups, int32_t beam_width, int32_t vocab, int32_t num_select) {
+    if (check_select(num_groups, beam_width, vocab, num_select) != SA_OK) return 0;
+    return select_layout(num_groups, beam_width, vocab, num_select).total;
+}
+
+static int select_impl(const void *logits, bool bf16, int64_t logits_stride, const float *scores,
+                       const int32_t *finished, int32_t num_groups, int32_t beam_width, int32_t vocab,
+                       int32_t num_select, int32_t eos_token, int32_t *tokens, int32_t *parents, float *scores_out,
+                       int32_t *finished_out, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_select(num_groups, beam_width, vocab, num_select);
+    if (rc) return rc;
+    if (eos_token < -1 || eos_token >= vocab || ((finished || finished_out) && eos_token < 0)) return SA_ERR_ARG;
+    if (logits_stride < vocab) return SA_ERR_ARG;
+    if (num_groups == 0) return SA_OK;
+    if (!logits || !scores || !tokens || !parents || !scores_out) return SA_ERR_ARG;
+    if (!aligned(logits, bf16 ? 2 : 4) || !aligned(scores, 4) || !aligned(scores_out, 4)) return SA_ERR_ARG;
+    const SelectLayout w = select_layout(num_groups, beam_width, vocab, num_select);
+    if (workspace == nullptr || workspace_bytes < w.total || !aligned(workspace, 256)) return SA_ERR_WORKSPACE;
+    const int sms = device_sm_count();
+    if (sms <= 0) return SA_ERR_CUDA;
+    // 32 values a thread where that gives every SM two CTAs, else 8, so that
+    // few rows spread over more SMs
+    const int64_t rows = static_cast<int64_t>(num_groups) * beam_width;
+    const bool large = rows * select_chunks(vocab, beam_select_chunk_values(true)) >= 2 * sms;
+    const int values = beam_select_chunk_values(large);
+    SelectParams p{};
+    p.logits = logits;
+    p.stride = logits_stride;
+    p.scores = scores;
+    p.finished = finished;
+    p.tokens = tokens;
+    p.parents = parents;
+    p.scores_out = scores_out;
+    p.finished_out = finished_out;
+    char *ws = static_cast<char *>(workspace);
+    p.counters = reinterpret_cast<int32_t *>(ws);
+    p.part_keys = reinterpret_cast<uint64_t *>(ws + w.keys_offset);
+    p.part_sums = reinterpret_cast<float2 *>(ws + w.sums_offset);
+    p.B = num_groups;
+    p.W = beam_width;
+    p.V = vocab;
+    p.K = num_select;
+    p.eos = eos_token;
+    // even chunks, in 16-byte groups
+    p.n_chunks = static_cast<int32_t>(select_chunks(vocab, values));
+    p.chunk = ((vocab + p.n_chunks - 1) / p.n_chunks + 7) / 8 * 8;
+    const bool rows_aligned = aligned(logits, 16) && logits_stride * (bf16 ? 2 : 4) % 16 == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_beam_select(p, bf16, large, rows_aligned, s) != cudaSuccess) return SA_ERR_CUDA;
+    return finish(s, nullptr);
+}
+
+int sa_beam_select(const float *logits, int64_t logits_stride, const float *scores, const int32_t *finished,
+                   int32_t num_groups, int32_t beam_width, int32_t vocab, int32_t num_select, int32_t eos_token,
+                   int32_t *tokens, int32_t *parents, float *scores_out, int32_t *finished_out, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    return select_impl(logits, false, logits_stride, scores, finished, num_groups, beam_width, vocab, num_select,
+                       eos_token, tokens, parents, scores_out, finished_out, workspace, workspace_bytes, stream);
+}
+
+int sa_beam_select_bf16(const uint16_t *logits, int64_t logits_stride, const float *scores, const int32_t *finished,
+                        int32_t num_groups, int32_t beam_width, int32_t vocab, int32_t num_select,
+                        int32_t eos_token, int32_t *tokens, int32_t *parents, float *scores_out,
+                        int32_t *finished_out, void *workspace, size_t workspace_bytes, void *stream) {
+    return select_impl(logits, true, logits_stride, scores, finished, num_groups, beam_width, vocab, num_select,
+                       eos_token, tokens, parents, scores_out, finished_out, workspace, workspace_bytes, stream);
+}
+
+static int reorder_impl(const sa_dims *dims, int32_t beam_width, const int32_t *parents, const int32_t *block_table,
+                        const int32_t *seq_lens, int32_t *block_table_out, void *k_pool, void *v_pool,
+                        float *k_scales, float *v_scales, int bits, int32_t *err_flag, void *stream) {
+    int rc = check_dims(dims);
+    if (rc) return rc;
+    const sa_dims &d = *dims;
+    if (beam_width <= 0 || d.num_seqs % beam_width != 0) return SA_ERR_ARG;
+    if (beam_width > kMaxBeamWidth) return SA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d.num_seqs) * d.num_kv_heads > INT32_MAX) return SA_ERR_UNSUPPORTED;
+    if (d.num_seqs == 0) return SA_OK;
+    if (!parents || !seq_lens || !k_pool || !v_pool || (bits != 16 && (!k_scales || !v_scales))) return SA_ERR_ARG;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return SA_ERR_ARG;
+    // every row of the new table is made from two rows of the old one
+    const int64_t entries = static_cast<int64_t>(d.num_seqs) * d.max_pages_per_seq;
+    if (entries > 0 && (!block_table || !block_table_out)) return SA_ERR_ARG;
+    if (block_table < block_table_out + entries && block_table_out < block_table + entries) return SA_ERR_ARG;
+    ReorderParams p{};
+    p.parents = parents;
+    p.table = block_table;
+    p.seq_lens = seq_lens;
+    p.table_out = block_table_out;
+    p.pools[0] = static_cast<char *>(k_pool);
+    p.pools[1] = static_cast<char *>(v_pool);
+    p.scales[0] = k_scales;
+    p.scales[1] = v_scales;
+    p.err = err_flag;
+    p.num_seqs = d.num_seqs;
+    p.W = beam_width;
+    p.Hkv = d.num_kv_heads;
+    p.num_pages = d.num_pages;
+    p.max_pages = d.max_pages_per_seq;
+    p.row_bytes = kHeadDim * bits / 8;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_beam_reorder(p, s) != cudaSuccess) return SA_ERR_CUDA;
+    return finish(s, err_flag);
+}
+
+int sa_beam_reorder(const sa_dims *dims, int32_t beam_width, const int32_t *parents, const int32_t *block_table,
+                    const int32_t *seq_lens, int32_t *block_table_out, uint16_t *k_pages, uint16_t *v_pages,
+                    int32_t *err_flag, void *stream) {
+    return reorder_impl(dims, beam_width, parents, block_table, seq_lens, block_table_out, k_pages, v_pages, nullptr,
+                        nullptr, 16, err_flag, stream);
+}
+
+int sa_beam_reorder_q8(const sa_dims *dims, int32_t beam_width, const int32_t *parents, const int32_t *block_table,
+                       const int32_t *seq_lens, int32_t *block_table_out, int8_t *k_codes, int8_t *v_codes,
+                       float *k_scales, float *v_scales, int32_t *err_flag, void *stream) {
+    return reorder_impl(dims, beam_width, parents, block_table, seq_lens, block_table_out, k_codes, v_codes, k_scales,
+                        v_scales, 8, err_flag, stream);
+}
+
+int sa_beam_reorder_q4(const sa_dims *dims, int32_t beam_width, const int32_t *parents, const int32_t *block_table,
+                       const int32_t *seq_lens, int32_t *block_table_out, uint8_t *k_codes, uint8_t *v_codes,
+                       float *k_scales, float *v_scales, int32_t *err_flag, void *stream) {
+    return reorder_impl(dims, beam_width, parents, block_table, seq_lens, block_table_out, k_codes, v_codes, k_scales,
+                        v_scales, 4, err_flag, stream);
+}
+
+// ---------------------------------------------------------------------------
 // Paged attention without any allocation by the caller or the library.
 //
 // Some callers cannot allocate device memory at all: a plugin that runs inside

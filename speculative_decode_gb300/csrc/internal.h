@@ -16,7 +16,9 @@ constexpr int kPageSize = 256;
 constexpr int kMaxQLen = 512;     // new tokens per sequence in one call (decode 1, verify k+1, prefill chunks)
 constexpr int kPlanMaxQLen = 16;  // with a shared-prefix plan
 constexpr int kMaxKMax = 15;
+constexpr int kMaxRopeHeads = 1 << 16;  // row offsets inside a token fit 32 bits
 
+constexpr int32_t kErrBitArg = 1 << SA_ERR_ARG;
 constexpr int32_t kErrBitPageOOB = 1 << SA_ERR_PAGE_OOB;
 constexpr int32_t kErrBitTimeout = 1 << SA_ERR_TIMEOUT;
 constexpr int32_t kErrBitQlen = 1 << SA_ERR_QLEN;
@@ -159,6 +161,58 @@ struct VerifyParams {
     int32_t B, k_max, V, n_chunks, chunk;
 };
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
+
+// Norm and rotation of query and key rows (rope.cu), into dense rows or pages.
+// Rows are heads of 128 bf16 values, packed in their token; strides are in
+// values from one token to the next.
+struct RopeParams {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    uint16_t *q_out, *k_out;      // k_out: dense keys (no pages)
+    int64_t q_out_stride, k_out_stride;
+    uint16_t *k_pages, *v_pages;  // bf16 pages
+    uint8_t *k_codes, *v_codes;   // or code pages and their scales
+    float *k_scales, *v_scales;
+    const float *inv_freq;        // [half]
+    const float *q_weight, *k_weight;  // nullable: no norm
+    const int32_t *positions;     // one a row; nullable with pages (the cache position)
+    const int32_t *block_table, *seq_lens, *q_lens;
+    int32_t *err;
+    float eps;
+    int32_t half, interleaved;    // pairs, and whether they are neighbours
+    int32_t B, Hq, Hkv, num_pages, max_pages, max_q_len, total_q;
+};
+// code_bits 0: dense keys; 16, 8, 4: pages of that kind
+cudaError_t launch_rope(const RopeParams &p, int code_bits, int num_tokens, cudaStream_t stream);
+
+// Beam search (beam.cu).
+constexpr int kMaxBeamWidth = 32;
+struct SelectParams {
+    const void *logits;       // [B * W] rows of V fp32 or bf16, `stride` values apart
+    int64_t stride;
+    const float *scores;      // [B][W]
+    const int32_t *finished;  // nullable [B][W]
+    int32_t *tokens, *parents;
+    float *scores_out;
+    int32_t *finished_out;    // nullable
+    uint64_t *part_keys;      // [B * W][n_chunks][K] picks of a chunk, best first (0: none)
+    float2 *part_sums;        // [B * W][n_chunks] maximum, sum of exp(x - maximum)
+    int32_t *counters;        // [B], zero between calls
+    int32_t B, W, V, K, eos, n_chunks, chunk;
+};
+// aligned: every row starts on a 16-byte boundary
+cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool large, bool aligned, cudaStream_t stream);
+int beam_select_chunk_values(bool large);  // values of a row that one CTA holds
+
+struct ReorderParams {
+    const int32_t *parents, *table, *seq_lens;
+    int32_t *table_out;
+    char *pools[2];           // rows of row_bytes, [num_pages][Hkv][256]
+    float *scales[2];         // nullable
+    int32_t *err;
+    int32_t num_seqs, W, Hkv, num_pages, max_pages, row_bytes;
+};
+cudaError_t launch_beam_reorder(const ReorderParams &p, cudaStream_t stream);
 
 // Driver entry point for tensor-map encoding (resolved once, no -lcuda).
 CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, void *base,

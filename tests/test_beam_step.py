@@ -1,0 +1,218 @@
+"""CPU checks of the beam-decoding step: pins of its fp64 definitions, and the
+refusals of the entry points (none needs a GPU)."""
+import ctypes
+import itertools
+import os
+import shutil
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import beam_step as ref
+
+needs_nvcc = pytest.mark.skipif(shutil.which("nvcc") is None and
+                                not os.path.exists("/usr/local/cuda/bin/nvcc"),
+                                reason="no CUDA toolkit")
+
+
+@pytest.fixture(scope="module")
+def sa():
+    from speculative_decode_gb300 import build
+    build.build()
+    import speculative_decode_gb300 as mod
+    mod.load_library()
+    return mod
+
+
+# ------------------------------------------------------------------------ pins
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rotary", [0, 16, 64, 128])
+def test_rotation_is_a_complex_product(rotary, interleaved):
+    rng = np.random.default_rng(rotary)
+    x = rng.standard_normal((5, 3, 128))
+    inv = 10000.0 ** (-np.arange(rotary // 2) / max(1, rotary // 2))
+    pos = np.array([0, 1, 7, 100000, -3])
+    y = ref.rope_rows(x, pos, inv, rotary, interleaved)
+    assert np.array_equal(y[0], x[0]) and np.array_equal(y[..., rotary:], x[..., rotary:])
+    a, b = (x[..., 0:rotary:2], x[..., 1:rotary:2]) if interleaved else (x[..., :rotary // 2], x[..., rotary // 2:rotary])
+    u, v = (y[..., 0:rotary:2], y[..., 1:rotary:2]) if interleaved else (y[..., :rotary // 2], y[..., rotary // 2:rotary])
+    z = (a + 1j * b) * np.exp(1j * pos[:, None] * inv)[:, None]
+    assert np.allclose(z.real, u, atol=1e-12) and np.allclose(z.imag, v, atol=1e-12)
+
+
+def test_rotated_products_depend_on_the_distance_alone():
+    rng = np.random.default_rng(1)
+    q, k = rng.standard_normal((2, 1, 1, 128))
+    inv = 10000.0 ** (-np.arange(64) / 64)
+    dots = [float((ref.rope_rows(q, [p], inv, 128) * ref.rope_rows(k, [p - 5], inv, 128)).sum()) for p in (5, 50, 9000)]
+    assert np.allclose(dots, dots[0], atol=1e-9)
+
+
+def test_norm_gives_unit_mean_square():
+    x = np.random.default_rng(2).standard_normal((4, 2, 128)) * 37
+    y = ref.rope_rows(x, np.arange(4), np.ones(64), 128, weight=np.ones(128), eps=1e-12)
+    assert np.allclose((y * y).mean(-1), 1)
+
+
+def test_selection_equals_brute_force_over_all_continuations():
+    rng = np.random.default_rng(3)
+    for W, V, K in itertools.product((1, 3), (1, 2, 9), (1, 3)):
+        if K > W * V:
+            continue
+        x, s = rng.standard_normal((W, V)), rng.standard_normal(W)
+        logp = torch.log_softmax(torch.from_numpy(x), -1).numpy() + s[:, None]
+        order = np.argsort(-logp.ravel(), kind="stable")[:K]
+        t, p, v = ref.beam_select(x, s, K)
+        assert np.array_equal(p * V + t, order) and np.allclose(v, logp.ravel()[order])
+
+
+def test_selection_hand_worked():
+    inf, nan = np.inf, np.nan
+    half = np.log(0.5)
+    # equal rows and scores: the lower beam, then the lower token
+    t, p, v = ref.beam_select(np.zeros((2, 2)), [0.0, 0.0], 3)
+    assert t.tolist() == [0, 1, 0] and p.tolist() == [0, 0, 1] and np.allclose(v, half)
+    # a finished beam offers its end token at its own score
+    t, p, v = ref.beam_select(np.zeros((2, 2)), [-0.1, -5.0], 2, finished=[1, 0], eos=1)
+    assert t.tolist() == [1, 0] and p.tolist() == [0, 1] and np.allclose(v, [-0.1, -5 + half])
+    # fewer continuations than wanted: the rest has no probability, in order
+    t, p, v = ref.beam_select(np.array([[-inf, 3.0, nan], [1.0, 2.0, -inf]]), [0.0, -inf], 4)
+    assert t.tolist() == [1, 0, 2, 1] and p.tolist() == [0, 0, 0, 1] and v.tolist() == [0.0, -inf, -inf, -inf]
+    # an infinite logit takes all the probability
+    t, p, v = ref.beam_select(np.array([[0.0, inf, 5.0]]), [-1.0], 1)
+    assert t.tolist() == [1] and v.tolist() == [-1.0]
+
+
+def test_reordered_tables_hold_each_parents_tokens():
+    rng = np.random.default_rng(4)
+    for W, T in ((4, 600), (5, 512), (3, 100), (8, 255)):
+        full = T // 256
+        shared = rng.integers(0, 9, size=(1, full))
+        own = np.arange(100, 100 + 2 * W).reshape(W, 2)
+        table = np.concatenate([np.repeat(shared, W, 0), own], 1)
+        content = {int(p): rng.integers(0, 1000, 256) for p in np.unique(table)}
+        before = [np.concatenate([content[int(p)] for p in row])[:T] for row in table]
+        parents = rng.integers(0, W, W)
+        new, copies = ref.beam_reorder(table, [T] * W, parents, W)
+        assert not {c[0] for c in copies} & {c[1] for c in copies}
+        for a, b, rows in copies:
+            content[b][:rows] = content[a][:rows]
+        for i in range(W):
+            assert np.array_equal(np.concatenate([content[int(p)] for p in new[i]])[:T], before[parents[i]])
+        assert sorted(new[:, full:].ravel()) == sorted(own.ravel())  # every own page belongs to one beam still
+
+
+# -------------------------------------------------------------------- refusals
+PTR = 1 << 20  # an address that no call reaches
+
+
+def rope_struct(sa, **kw):
+    from speculative_decode_gb300 import _lib
+    f = {"inv_freq": PTR, "q_weight": None, "k_weight": None, "eps": 1e-6, "rotary_dim": 128, "interleaved": 0} | kw
+    return ctypes.byref(_lib._RopeStruct(*[f[n] for n, _ in _lib._RopeStruct._fields_]))
+
+
+@needs_nvcc
+def test_qk_norm_rope_refuses(sa):
+    lib = sa.load_library()
+
+    def call(rope, n=3, hq=4, hk=2, hd=128, q=PTR, qs=512, k=PTR, ks=256, pos=PTR, qo=PTR, qos=512, ko=PTR, kos=256):
+        return lib.sa_qk_norm_rope(rope, n, hq, hk, hd, q, qs, k, ks, pos, qo, qos, ko, kos, None)
+
+    ok = rope_struct(sa)
+    assert call(None) == 1
+    assert call(ok, hd=64) == 2
+    assert call(rope_struct(sa, rotary_dim=24)) == 2
+    assert call(rope_struct(sa, rotary_dim=33)) == 1
+    assert call(rope_struct(sa, rotary_dim=144)) == 1
+    assert call(rope_struct(sa, rotary_dim=-16)) == 1
+    assert call(rope_struct(sa, inv_freq=None)) == 1
+    assert call(rope_struct(sa, q_weight=PTR + 4)) == 1
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(rope_struct(sa, k_weight=PTR, eps=eps)) == 1
+    for bad in (dict(n=-1), dict(hq=-1), dict(hk=-1), dict(q=None), dict(q=PTR + 8), dict(qs=511), dict(qs=516),
+                dict(qs=0), dict(k=None), dict(ks=128), dict(pos=None), dict(qo=None), dict(qos=504), dict(ko=PTR + 2)):
+        assert call(ok, **bad) == 1, bad
+    assert call(ok, hq=1 << 17, qs=1 << 24, qos=1 << 24) == 2
+    assert call(ok, n=0) == 0 and call(ok, hq=0, hk=0) == 0  # nothing to do
+
+
+@needs_nvcc
+def test_kv_append_rope_refuses(sa):
+    lib = sa.load_library()
+    ok = rope_struct(sa)
+    for name, pools in (("sa_kv_append_rope", 2), ("sa_kv_append_rope_q8", 4), ("sa_kv_append_rope_q4", 4)):
+        def call(rope=ok, dims=None, q=PTR, qs=1024, k=PTR, ks=256, v=PTR, vs=256, qo=PTR, pool=None, bt=PTR, sl=PTR, ql=PTR):
+            d = dims or sa.dims_for(2, 8, 2, 4, 2, 2, 1)
+            return getattr(lib, name)(ctypes.byref(d), rope, q, qs, k, ks, v, vs, qo, *(pool or [PTR] * pools), bt, sl, ql,
+                                      None, None, None)
+
+        assert call(rope=None) == 1
+        assert call(dims=sa.dims_for(2, 8, 3, 4, 2, 2, 1)) == 1
+        assert call(dims=sa.dims_for(2, 8, 2, 4, 2, 2, 513)) == 2
+        assert call(dims=sa.dims_for(2, 8, 2, 4, 2, 2, 1, head_dim=64)) == 2
+        for bad in (dict(q=None), dict(qo=None), dict(qs=1000), dict(k=None), dict(k=PTR + 4), dict(ks=260), dict(v=None),
+                    dict(vs=128), dict(qo=PTR + 8), dict(bt=None), dict(sl=None), dict(ql=None)):
+            assert call(**bad) == 1, bad
+        for i in range(pools):
+            assert call(pool=[PTR if j != i else None for j in range(pools)]) == 1
+        assert call(pool=[PTR + 8] + [PTR] * (pools - 1)) == 1
+        assert call(dims=sa.dims_for(0, 8, 2, 4, 2, 0, 1)) == 0
+
+
+@needs_nvcc
+def test_beam_select_refuses(sa):
+    lib = sa.load_library()
+    assert sa.beam_select_workspace_size(2, 4, 1000, 4) > 0
+    for bad in ((-1, 4, 1000, 4), (2, 0, 1000, 4), (2, 4, 0, 4), (2, 4, 1000, 0), (2, 33, 1000, 4), (2, 4, 1000, 33),
+                (2, 2, 3, 7), (16385, 1, 10, 1), (2, 4, (1 << 26) + 1, 4)):
+        assert sa.beam_select_workspace_size(*bad) == 0, bad
+    for name, size in (("sa_beam_select", 4), ("sa_beam_select_bf16", 2)):
+        def call(x=PTR, stride=1000, s=PTR, fin=None, B=2, W=4, V=1000, K=4, eos=-1, t=PTR, p=PTR, so=PTR, fo=None, ws=PTR,
+                 nws=1 << 30):
+            return getattr(lib, name)(x, stride, s, fin, B, W, V, K, eos, t, p, so, fo, ws, nws, None)
+
+        for bad in (dict(B=-1), dict(W=0), dict(V=0), dict(K=0), dict(K=9, W=1, V=8, stride=8), dict(stride=999), dict(x=None),
+                    dict(s=None), dict(t=None), dict(p=None), dict(so=None), dict(x=PTR + size // 2), dict(eos=1000),
+                    dict(eos=-2), dict(fin=PTR), dict(fo=PTR)):
+            assert call(**bad) == 1, bad
+        for bad in (dict(W=33), dict(K=33), dict(B=16385), dict(V=(1 << 26) + 8, stride=1 << 27)):
+            assert call(**bad) == 2, bad
+        for bad in (dict(ws=None), dict(ws=PTR + 128), dict(nws=sa.beam_select_workspace_size(2, 4, 1000, 4) - 1)):
+            assert call(**bad) == 6, bad
+        assert call(B=0) == 0
+
+
+@needs_nvcc
+def test_beam_reorder_refuses(sa):
+    lib = sa.load_library()
+    for name, pools in (("sa_beam_reorder", 2), ("sa_beam_reorder_q8", 4), ("sa_beam_reorder_q4", 4)):
+        def call(W=4, dims=None, pa=PTR, bt=PTR, sl=PTR, bo=2 * PTR, pool=None):
+            d = dims or sa.dims_for(8, 8, 2, 40, 3, 8, 1)
+            return getattr(lib, name)(ctypes.byref(d), W, pa, bt, sl, bo, *(pool or [PTR] * pools), None, None)
+
+        for bad in (dict(W=0), dict(W=3), dict(pa=None), dict(bt=None), dict(sl=None), dict(bo=None), dict(bo=PTR),
+                    dict(bo=PTR + 8 * 3 * 4 - 4), dict(bo=PTR - 8 * 3 * 4 + 4)):
+            assert call(**bad) == 1, bad
+        assert call(W=64, dims=sa.dims_for(64, 8, 2, 40, 3, 64, 1)) == 2
+        for i in range(pools):
+            assert call(pool=[PTR if j != i else None for j in range(pools)]) == 1
+        assert call(dims=sa.dims_for(0, 8, 2, 40, 3, 0, 1)) == 0
+
+
+@needs_nvcc
+def test_binding_refuses_host_tensors(sa):
+    z = torch.zeros
+    with pytest.raises(ValueError, match="inv_freq"):
+        sa.Rope(z(64))
+    with pytest.raises(ValueError, match="inv_freq is missing"):
+        sa.Rope(None)
+    with pytest.raises(ValueError, match="logits"):
+        sa.beam_select(z(1, 2, 10), z(1, 2), z(1, 2, dtype=torch.int32), z(1, 2, dtype=torch.int32), z(1, 2),
+                       z(1 << 20, dtype=torch.uint8))
+    d = sa.dims_for(2, 8, 2, 4, 2, 2, 1)
+    pool = z(4, 2, 256, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="page pool"):
+        sa.beam_reorder(d, 2, z(2, dtype=torch.int32), z(2, 2, dtype=torch.int32), z(2, dtype=torch.int32),
+                        z(2, 2, dtype=torch.int32), pool, pool)

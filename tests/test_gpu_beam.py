@@ -1,0 +1,384 @@
+"""GPU parity of beam_select and beam_reorder with their definitions, and a
+whole decoding loop of them with the rotating append and paged attention.
+
+Tokens and parents have to be equal. The inputs' values are either apart by
+more than the accuracy of a row's sum (checked: GAP), or equal by construction.
+Scores: one rounding to fp32 (2^-24 of the value) and the error of the sum's
+logarithm: 32 terms a thread with an exponential of two ulp and a rounded
+argument (2^-22 and 2^-24 of |x - max| log2 e <= 2^7 where a term matters,
+averaged over the terms), tree sums of 13 levels (13 * 2^-24): below 2^-19.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import speculative_decode_gb300 as sa
+import workloads as wl
+from gpu_path import dev_tensor
+from oracle import beam_step as ref
+
+pytestmark = pytest.mark.gpu
+SUM = 2.0 ** -19
+GAP = 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decode_gb300 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+def run_select(logits, scores, K, finished=None, eos=-1, ws=None, offset=0, pad=0):
+    """logits: torch [B, W, V] (host). The rows go `offset` values behind an
+    aligned address, V + pad values apart."""
+    B, W, V = logits.shape
+    buf = torch.full((offset + B * W * (V + pad) + 8,), 99.0, dtype=logits.dtype, device="cuda")
+    x = buf[offset:offset + B * W * (V + pad)].view(B, W, V + pad)[..., :V]
+    x.copy_(logits)
+    if ws is None:
+        ws = torch.zeros(sa.beam_select_workspace_size(B, W, V, K), dtype=torch.uint8, device="cuda")
+    i32 = lambda: torch.full((B, K), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    tok, par, sc, fo = i32(), i32(), torch.zeros(B, K, device="cuda"), i32() if finished is not None else None
+    sa.beam_select(x, dev_tensor(scores.astype(np.float32)), tok, par, sc, ws, finished=None if finished is None else
+                   dev_tensor(finished.astype(np.int32)), finished_out=fo, eos_token=eos)
+    torch.cuda.synchronize()
+    return tok.cpu().numpy(), par.cpu().numpy(), sc.cpu().numpy(), None if fo is None else fo.cpu().numpy()
+
+
+def check_select(logits, scores, K, finished=None, eos=-1, gap=True, **kw):
+    tok, par, sc, fo = run_select(logits, scores, K, finished, eos, **kw)
+    x = logits.float().numpy()
+    for g in range(len(x)):
+        t, p, v = ref.beam_select(x[g], scores[g].astype(np.float32), min(K + 1, x[g].size), None if finished is None else finished[g], eos)
+        if gap:  # the inputs tell the values of different beams apart
+            near = np.flatnonzero(np.diff(v) > -GAP) if len(v) > 1 else []
+            assert all(p[i] == p[i + 1] or v[i + 1] == -np.inf for i in near), "inputs too close"
+        t, p, v = t[:K], p[:K], v[:K]
+        assert np.array_equal(tok[g], t) and np.array_equal(par[g], p), (g, tok[g], t, par[g], p)
+        fine = np.isfinite(v)
+        with np.errstate(over="ignore"):
+            v32 = v.astype(np.float32)
+        assert np.array_equal(np.isfinite(sc[g]), np.isfinite(v32)) and (sc[g][~np.isfinite(v32)] == v32[~np.isfinite(v32)]).all()
+        fine = np.isfinite(v32)
+        assert (np.abs(sc[g][fine] - v[fine]) <= 2.0 ** -24 * np.abs(v[fine]) + SUM).all()
+        if fo is not None:
+            assert np.array_equal(fo[g], ((finished[g][p] != 0) | (t == eos)).astype(np.int32))
+
+
+def draws(seed, B, W, V, dtype=torch.float32):
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy((rng.standard_normal((B, W, V)) * 3).astype(np.float32)).to(dtype)
+    return x, -20 * rng.random((B, W)), rng
+
+
+@pytest.mark.parametrize("B,W,V,K", [
+    (1, 1, 1, 1), (1, 1, 2, 2), (2, 3, 1, 3), (3, 4, 7, 5), (1, 8, 33, 32), (2, 32, 9, 32), (1, 4, 32000, 4), (1, 32, 4097, 32),
+    (5, 2, 2048, 4), (2, 3, 2049, 6), (1, 3, 8192, 3), (3, 7, 50257, 14), (13, 5, 50257, 10), (1, 1, 300001, 9), (40, 8, 32000, 8),
+    (4, 32, 20011, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_select(B, W, V, K, dtype):
+    x, s, _ = draws(B * 100 + W + V, B, W, V, dtype)
+    check_select(x, s, K)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset,pad", [(1, 0), (0, 3), (8, 8), (3, 5), (0, 1111)])
+def test_select_of_rows_at_any_address(dtype, offset, pad):
+    x, s, _ = draws(7, 3, 4, 9000, dtype)
+    check_select(x, s, 8, offset=offset, pad=pad)
+
+
+@pytest.mark.parametrize("V", [1, 5, 3000, 128256])
+def test_select_with_finished_beams(V):
+    for seed, K in ((0, 6), (1, 3), (2, 12)):
+        x, s, rng = draws(seed, 4, 6, V)
+        fin = (rng.random((4, 6)) < 0.4).astype(np.int32)
+        fin[0] = 1                                # a group that is done
+        if K <= 6 * V:
+            check_select(x, s, K, finished=fin, eos=int(rng.integers(0, V)))
+
+
+def test_select_first_step():
+    x, s, _ = draws(3, 3, 5, 1000)
+    s[:] = -np.inf
+    s[:, 0] = 0
+    check_select(x, s, 5)
+    # a vocabulary with fewer tokens than beams: the rest has no probability
+    x, s, _ = draws(4, 2, 5, 3)
+    s[:] = -np.inf
+    s[0, 0] = 0
+    check_select(x, s, 5)
+    check_select(x, s, 12)
+
+
+@pytest.mark.parametrize("low", [-np.inf, np.nan, float(np.finfo(np.float32).min), -1e4])
+@pytest.mark.parametrize("V", [40, 5000, 70000])
+def test_select_of_masked_vocabularies(V, low):
+    """All but a few tokens masked, in one row all."""
+    rng = np.random.default_rng(V)
+    for left in (0, 1, 3, 20):
+        x = np.full((2, 3, V), low, np.float32)
+        for g in range(2):
+            for w in range(3):
+                x[g, w, rng.choice(V, left, replace=False)] = rng.standard_normal(left) * 3
+        x[1, 1] = low
+        s = -5 * rng.random((2, 3))
+        check_select(torch.from_numpy(x), s, 8, gap=False)
+
+
+def test_select_ties():
+    """Equal values: the lower beam, in a beam the larger logit, then the lower token."""
+    rng = np.random.default_rng(9)
+    for V in (4, 100, 4099, 50257, 128256):
+        row = torch.from_numpy(rng.integers(-3, 3, V).astype(np.float32))
+        row[rng.integers(0, V)] = -0.0
+        x = row.expand(2, 6, V).contiguous()      # equal beams, heavy ties inside
+        for K in (4, 7, 24):
+            check_select(x, np.full((2, 6), -1.5), K, gap=False)
+        check_select(torch.zeros(1, 3, V), np.zeros((1, 3)), 12, gap=False)
+        check_select(torch.randn(V, generator=torch.Generator().manual_seed(V)).expand(1, 4, V).contiguous(), np.zeros((1, 4)), 4, gap=False)
+
+
+def test_select_of_sorted_and_striped_rows():
+    """Orders in which many values pass a chunk's threshold."""
+    V = 40000
+    up = torch.arange(V, dtype=torch.float32) / 1000
+    stripes = torch.where(torch.arange(V) % 1024 < 128, -50.0, torch.arange(V) % 7 * 1.0)
+    empty = torch.where(torch.arange(V) % 1024 < 128, -torch.inf, torch.arange(V) % 7919 * 0.001)
+    runs = torch.where(torch.arange(V) % 256 < 32, -torch.inf, torch.arange(V) % 7919 * 0.001)
+    x = torch.stack([up, up.flip(0), stripes, empty, runs])[None]
+    s = np.array([[-1.0, -2.1, -3.3, -4.7, -5.9]])
+    for K in (5, 10, 32):
+        check_select(x, s, K, gap=False)
+        check_select(x, s, K, gap=False, offset=1)
+
+
+def test_select_of_infinite_and_odd_values():
+    x, s, _ = draws(11, 2, 4, 6000)
+    x[0, 0, 17] = float("inf")
+    x[0, 1, 100:105] = float("nan")
+    x[0, 2] = -torch.inf
+    x[1, 1] *= 1e37
+    x[1, 2, 5] = 3.0e38
+    s[1, 3] = np.nan
+    s[0, 3] = -3e38
+    check_select(x, s, 8, gap=False)
+
+
+def test_select_in_place_on_one_workspace_and_in_a_graph():
+    """scores and finished updated in place; one workspace for calls of other
+    shapes; repeated and replayed calls give the same."""
+    x, s, rng = draws(21, 3, 4, 30000)
+    fin = (rng.random((3, 4)) < 0.2).astype(np.int32)
+    want = run_select(x, s, 4, fin, 77)
+    ws = torch.zeros(sa.beam_select_workspace_size(40, 8, 50000, 8), dtype=torch.uint8, device="cuda")
+    for B, W, V, K in ((40, 8, 50000, 8), (1, 2, 100, 2), (3, 32, 9000, 32), (40, 8, 50000, 8)):
+        y, sy, _ = draws(B + V, B, W, V)
+        check_select(y, sy, K, ws=ws)
+    X, S, F = x.cuda(), dev_tensor(s.astype(np.float32)), dev_tensor(fin)
+    tok, par = (torch.zeros(3, 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    call = lambda: sa.beam_select(X, S, tok, par, S, ws, finished=F, finished_out=F, eos_token=77)  # noqa: E731
+    start = S.clone(), F.clone()
+    call()
+    for got, w in zip((tok, par, S, F), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        S.copy_(start[0])
+        F.copy_(start[1])
+        tok.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip((tok, par, S, F), want):
+            assert np.array_equal(got.cpu().numpy(), w)
+
+
+def test_select_on_two_streams_at_once():
+    cases = [draws(31 + i, 8, 4, 60000) for i in range(2)]
+    want = [run_select(x, s, 4) for x, s, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    state = []
+    for x, s, _ in cases:
+        state.append((x.cuda(), dev_tensor(s.astype(np.float32)), *(torch.zeros(8, 4, dtype=torch.int32, device="cuda") for _ in range(2)),
+                      torch.zeros(8, 4, device="cuda"), torch.zeros(sa.beam_select_workspace_size(8, 4, 60000, 4), dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, stream in zip(state, streams):
+            sa.beam_select(*st, stream=stream)
+    torch.cuda.synchronize()
+    for st, w in zip(state, want):
+        for got, e in zip(st[2:5], w):
+            assert np.array_equal(got.cpu().numpy(), e)
+
+
+# --------------------------------------------------------------------- reorder
+def reorder_case(seed, groups, W, T, hkv=2, spare=2, kind="bf16"):
+    rng = np.random.default_rng(seed)
+    full = T // 256
+    pages = groups * (full + spare * W) + 2
+    free = rng.permutation(pages)
+    table = np.empty((groups, W, full + spare), np.int32)
+    table[..., :full] = free[:groups * full].reshape(groups, 1, full)
+    table[..., full:] = free[groups * full:groups * (full + spare * W)].reshape(groups, W, spare)
+    shape = (pages, hkv, 256)
+    if kind == "bf16":
+        pool = [rng.integers(0, 65536, (*shape, 128)).astype(np.uint16) for _ in range(2)]
+    else:
+        pool = [rng.integers(0, 256, (*shape, 128 if kind == "q8" else 64)).astype(np.uint8) for _ in range(2)]
+        pool = [p.view(np.int8) for p in pool] if kind == "q8" else pool
+        pool += [rng.random(shape).astype(np.float32) for _ in range(2)]
+    return rng, table.reshape(groups * W, -1), np.full(groups * W, T, np.int32), pool, pages
+
+
+def run_reorder(kind, W, table, lens, pool, pages, parents, hkv=2):
+    d = sa.dims_for(len(lens), 4 * hkv, hkv, pages, table.shape[1], len(lens), 1)
+    dev = [dev_tensor(p) for p in pool]
+    out = torch.full(table.shape, -9, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fn = {"bf16": sa.beam_reorder, "q8": sa.beam_reorder_q8, "q4": sa.beam_reorder_q4}[kind]
+    fn(d, W, dev_tensor(parents), dev_tensor(table), dev_tensor(lens), out, *dev, err_flag=err)
+    torch.cuda.synchronize()
+    return out.cpu().numpy(), [t.cpu().numpy().view(p.dtype) for t, p in zip(dev, pool)], int(err.item())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8", "q4"])
+@pytest.mark.parametrize("groups,W,T,hkv", [(1, 1, 300, 1), (1, 2, 1, 8), (3, 4, 256, 2), (2, 5, 255, 3), (4, 8, 1000, 2), (2, 32, 515, 1),
+                                            (7, 3, 0, 2), (1, 16, 511, 5)])
+def test_reorder(kind, groups, W, T, hkv):
+    rng, table, lens, pool, pages = reorder_case(groups + W + T, groups, W, T, hkv, kind=kind)
+    for how in range(4):
+        parents = {0: rng.integers(0, W, groups * W), 1: np.zeros(groups * W, int), 2: np.tile(np.arange(W)[::-1], groups),
+                   3: np.full(groups * W, W - 1)}[how].astype(np.int32)
+        out, got, err = run_reorder(kind, W, table, lens, pool, pages, parents, hkv)
+        new, copies = ref.beam_reorder(table, lens, parents, W)
+        assert err == 0 and np.array_equal(out, new)
+        for g, p in zip(got, pool):
+            want = p.copy()
+            for a, b, rows in copies:
+                want[b, :, :rows] = p[a, :, :rows]
+            assert np.array_equal(g, want)
+
+
+def test_reorder_flags_bad_groups_and_pages():
+    rng, table, lens, pool, pages = reorder_case(5, 3, 4, 300)
+    good = np.array([0, 0, 1, 1, 2, 2, 2, 3, 0, 0, 0, 0], np.int32)
+    for value, bit in ((4, 1), (-1, 1)):
+        parents = good.copy()
+        parents[5] = value
+        out, got, err = run_reorder("bf16", 4, table, lens, pool, pages, parents)
+        assert err == 1 << bit
+        parents = np.concatenate([good[:4], good[8:]])
+        rest = np.r_[0:4, 8:12]
+        new, copies = ref.beam_reorder(table[rest], lens[rest], parents, 4)
+        assert np.array_equal(out[rest], new)
+        for g, p in zip(got, pool):
+            want = p.copy()
+            for a, b, rows in copies:
+                want[b, :, :rows] = p[a, :, :rows]
+            assert np.array_equal(g, want)
+    for change in (lambda s: s.__setitem__(6, 301), lambda s: s.__setitem__(slice(4, 8), -1), lambda s: s.__setitem__(slice(4, 8), 769)):
+        odd = lens.copy()
+        change(odd)
+        assert run_reorder("bf16", 4, table, odd, pool, pages, good)[2] == 1 << 7
+    for value in (-1, pages):
+        odd = table.copy()
+        odd[0, 1] = value                            # the page that beam 1 of group 0 continues
+        out, got, err = run_reorder("bf16", 4, odd, lens, pool, pages, good)
+        assert err == 1 << 3
+    # entries behind the one that is copied may be unset
+    odd = table.copy()
+    odd[:, 2:] = -1
+    out, got, err = run_reorder("bf16", 4, odd, lens, pool, pages, good)
+    assert err == 0 and np.array_equal(out, ref.beam_reorder(odd, lens, good, 4)[0])
+
+
+def test_reorder_binding_refuses():
+    rng, table, lens, pool, pages = reorder_case(6, 2, 4, 300)
+    d = sa.dims_for(8, 8, 2, pages, table.shape[1], 8, 1)
+    dev = [dev_tensor(p) for p in pool]
+    t, l, p = dev_tensor(table), dev_tensor(lens), torch.zeros(8, dtype=torch.int32, device="cuda")
+    for args in ((4, p[:7], t, l, t.clone()), (4, p, t, l, t[:, :2]), (4, p.long(), t, l, t.clone()), (4, p, t, l[:4], t.clone())):
+        with pytest.raises(ValueError):
+            sa.beam_reorder(d, *args, *dev)
+    for W in (3, 0):
+        with pytest.raises(sa.SpecAttnError):
+            sa.beam_reorder(d, W, p, t, l, t.clone(), *dev)
+    with pytest.raises(sa.SpecAttnError):        # the new table is not made in place
+        sa.beam_reorder(d, 4, p, t, l, t, *dev)
+
+
+# -------------------------------------------------------------------- the loop
+@pytest.mark.parametrize("W", [3, 4])
+def test_beam_decoding_loop_on_pages(W):
+    """Steps of rotating append, paged attention, selection and reordering over
+    a page boundary, against the same search on dense caches in fp64: every
+    beam's attention output is that of its own whole history."""
+    rng = np.random.default_rng(70 + W)
+    B, Hq, Hkv, V, T0, steps = 2, 8, 2, 500, 250, 12
+    N = B * W
+    inv = (10000.0 ** (-np.arange(64) / 64)).astype(np.float32)
+    wq, wk = ((rng.random(128) + 0.5).astype(np.float32) for _ in range(2))
+    rope = sa.Rope(dev_tensor(inv), q_weight=dev_tensor(wq), k_weight=dev_tensor(wk))
+    pages = N * 3 + 1
+    tables = [torch.from_numpy(rng.permutation(pages)[:N * 3].reshape(N, 3).astype(np.int32)).cuda()]
+    tables.append(torch.zeros_like(tables[0]))
+    kp, vp = (torch.zeros(pages, Hkv, 256, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(torch.bfloat16)  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = torch.full((N,), T0, dtype=torch.int32, device="cuda")
+    rows = lambda x, pos, w: wl.bf16_to_f32(wl.bf16_bits(ref.rope_rows(x, pos, inv, 128, weight=w).astype(np.float32))).astype(np.float64)  # noqa: E731
+
+    # prompt: the same T0 tokens for all beams of a group
+    prompt = bf(B, T0, 2 * Hkv, 128).repeat_interleave(W, 0)
+    d = sa.dims_for(N, Hq, Hkv, pages, 3, N * T0, T0)
+    flat = prompt.reshape(N * T0, 2 * Hkv, 128).cuda()
+    sa.kv_append_rope(d, rope, None, flat[:, :Hkv], flat[:, Hkv:], None, kp, vp, tables[0], lens, lens, err_flag=err)
+    pv = prompt.double().numpy()
+    ks = [rows(pv[n, :, :Hkv], np.arange(T0), wk) for n in range(N)]
+    vs = [pv[n, :, Hkv:] for n in range(N)]
+
+    d = sa.dims_for(N, Hq, Hkv, pages, 3, N, 1)
+    one = torch.ones(N, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(sa.paged_attn_workspace_size(d), dtype=torch.uint8, device="cuda")
+    bws = torch.zeros(sa.beam_select_workspace_size(B, W, V, W), dtype=torch.uint8, device="cuda")
+    scores = torch.full((B, W), -torch.inf, device="cuda")
+    scores[:, 0] = 0
+    finished = torch.zeros(B, W, dtype=torch.int32, device="cuda")
+    tok, par = (torch.zeros(B, W, dtype=torch.int32, device="cuda") for _ in range(2))
+    q_out, out = (torch.zeros(N, Hq, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for step in range(steps):
+        qkv, logits = bf(N, Hq + 2 * Hkv, 128), torch.from_numpy((rng.standard_normal((B, W, V)) * 3).astype(np.float32))
+        if step == 4:
+            logits[0, :, 7] = 30.0            # group 0 finishes a beam
+        x, lg = qkv.cuda(), logits.cuda()
+        lens += 1
+        sa.kv_append_rope(d, rope, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], q_out, kp, vp, tables[0], lens, one, err_flag=err)
+        sa.paged_attn(d, q_out, kp, vp, tables[0], lens, one, 128 ** -0.5, out, ws, err_flag=err)
+        s0, f0 = scores.cpu().numpy(), finished.cpu().numpy()
+        sa.beam_select(lg, scores, tok, par, scores, bws, finished=finished, finished_out=finished, eos_token=7)
+        sa.beam_reorder(d, W, par, tables[0], lens, tables[1], kp, vp, err_flag=err)
+        tables.reverse()
+        # the same on dense caches
+        xv, pos = qkv.double().numpy(), [T0 + step]
+        ks = [np.concatenate([ks[n], rows(xv[n:n + 1, Hq:Hq + Hkv], pos, wk)]) for n in range(N)]
+        vs = [np.concatenate([vs[n], xv[n:n + 1, Hq + Hkv:]]) for n in range(N)]
+        got = out.double().cpu().numpy()
+        for n in range(N):
+            q = rows(xv[n:n + 1, :Hq], pos, wq)[0].reshape(Hkv, Hq // Hkv, 128)
+            a = np.einsum("hgd,thd->hgt", q, ks[n]) * 128 ** -0.5
+            a = np.exp(a - a.max(-1, keepdims=True))
+            want = np.einsum("hgt,thd->hgd", a / a.sum(-1, keepdims=True), vs[n]).reshape(Hq, 128)
+            # the attention's stated tolerance; a rounding of q or k to the other side moves a score by 2^-8
+            assert np.abs(got[n] - want).max() <= 2e-2 and np.abs(got[n] - want).mean() <= 2e-3
+        parents = par.cpu().numpy()
+        for g in range(B):
+            t, p, v = ref.beam_select(logits[g].numpy(), s0[g], W, f0[g], 7)
+            assert np.array_equal(tok[g].cpu().numpy(), t) and np.array_equal(parents[g], p)
+        order = [g * W + int(p) for g in range(B) for p in parents[g]]
+        ks, vs = [ks[n] for n in order], [vs[n] for n in order]
+    assert int(err.item()) == 0
+    assert finished[0].any()

@@ -1,0 +1,363 @@
+"""GPU parity of qk_norm_rope and the kv_append_rope calls with their fp64
+definitions.
+
+Tolerance of a rotated value: one rounding to bf16 (half a step, 2^-8 of the
+value) and the fp32 work before it. The latter, relative to |a| + |b| of the
+rotated pair: the norm's sum and factor about ten roundings (10 * 2^-24), the
+angle's fraction of a turn one (pi * 2^-24, and 2^-53 of up to 2^29 turns),
+sin and cos two ulp (2^-23), three products and a sum (2 * 2^-24); together
+below 2^-19.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import speculative_decode_gb300 as sa
+import workloads as wl
+from gpu_path import dev_tensor
+from oracle import beam_step as ref
+
+pytestmark = pytest.mark.gpu
+WORK = 2.0 ** -19
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decode_gb300 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+def frequencies(rotary, base=500000.0):
+    half = rotary // 2
+    return (base ** (-np.arange(half) / max(1, half))).astype(np.float32)
+
+
+def make_rope(rng, rotary=128, interleaved=False, norm=True, eps=1e-6):
+    inv = frequencies(rotary)
+    w = [(rng.random(128) + 0.5).astype(np.float32) if norm else None for _ in range(2)]
+    h = sa.Rope(dev_tensor(inv) if rotary else None, rotary_dim=rotary, interleaved=interleaved,
+                q_weight=dev_tensor(w[0]) if norm else None, k_weight=dev_tensor(w[1]) if norm else None, eps=eps)
+    return h, lambda x, pos, side: (ref.rope_rows(x, pos, inv, rotary, interleaved, w[side], eps),
+                                    ref.pair_size(ref.rope_rows(x, pos, inv, 0, weight=w[side], eps=eps), rotary, interleaved))
+
+
+def assert_rows(got, want, size, what=""):
+    """bf16 rows against fp64 rows."""
+    g = got.detach().double().cpu().numpy()
+    assert g.shape == want.shape
+    bad = ~(np.abs(g - want) <= 2.0 ** -8 * np.abs(want) + WORK * size)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst {np.abs(g - want).max()}"
+
+
+def bf16(rng, *shape):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("tokens,hq,hkv,rotary,interleaved,norm", [
+    (1, 1, 1, 128, False, True), (1, 32, 8, 128, False, True), (3, 5, 1, 16, True, False), (17, 64, 8, 64, True, True),
+    (130, 32, 8, 96, False, True), (33, 7, 7, 80, False, False), (9, 128, 8, 32, False, True), (257, 8, 2, 128, True, True),
+    (5, 49, 3, 0, False, True)])
+def test_dense_rows(tokens, hq, hkv, rotary, interleaved, norm):
+    rng = np.random.default_rng(tokens + hq)
+    rope, want = make_rope(rng, rotary, interleaved, norm)
+    qkv = bf16(rng, tokens, hq + 2 * hkv, 128).cuda()     # views of one projection's output
+    q, k = qkv[:, :hq], qkv[:, hq:hq + hkv]
+    pos = rng.integers(0, 200000, tokens).astype(np.int32)
+    pos[:1] = 0
+    q_out, k_out = torch.zeros(tokens, hq, 128, dtype=torch.bfloat16).cuda(), torch.zeros(tokens, hkv, 128, dtype=torch.bfloat16).cuda()
+    kept = qkv.clone()
+    sa.qk_norm_rope(rope, q, k, dev_tensor(pos), q_out, k_out)
+    torch.cuda.synchronize()
+    assert torch.equal(qkv, kept)
+    assert_rows(q_out, *want(q.float().cpu().numpy(), pos, 0), "q")
+    assert_rows(k_out, *want(k.float().cpu().numpy(), pos, 1), "k")
+
+
+def test_far_and_negative_positions():
+    rng = np.random.default_rng(5)
+    rope, want = make_rope(rng, norm=False)
+    pos = np.array([2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -7, 1 << 20, 10 ** 9 + 7], np.int32)
+    q = bf16(rng, 6, 4, 128).cuda()
+    out = torch.empty_like(q)
+    sa.qk_norm_rope(rope, q, None, dev_tensor(pos), out, None)
+    assert_rows(out, *want(q.float().cpu().numpy(), pos, 0))
+
+
+def test_in_place_inside_the_projection_and_one_side_alone():
+    rng = np.random.default_rng(6)
+    rope, want = make_rope(rng)
+    qkv = bf16(rng, 37, 12, 128).cuda()
+    before = qkv.clone()
+    pos = np.arange(37, dtype=np.int32)
+    sa.qk_norm_rope(rope, qkv[:, :8], qkv[:, 8:10], dev_tensor(pos), qkv[:, :8], qkv[:, 8:10])
+    assert_rows(qkv[:, :8], *want(before[:, :8].float().cpu().numpy(), pos, 0))
+    assert_rows(qkv[:, 8:10], *want(before[:, 8:10].float().cpu().numpy(), pos, 1))
+    assert torch.equal(qkv[:, 10:], before[:, 10:])
+    k = before[:, 8:10].contiguous()
+    out = torch.zeros_like(k)
+    sa.qk_norm_rope(rope, None, k, dev_tensor(pos), None, out)
+    assert torch.equal(out, qkv[:, 8:10])
+
+
+def test_rows_of_extreme_values():
+    """Zero rows, rows whose squares pass 32 bits, infinities and NaN."""
+    rng = np.random.default_rng(7)
+    rope, want = make_rope(rng, rotary=64)
+    q = bf16(rng, 4, 1, 128)
+    q[0] = 0
+    q[1] *= 1e38 / q[1].abs().max()
+    q[2] *= 1e-30
+    q[3] *= 1e25
+    pos = np.array([3, 4, 5, 6], np.int32)
+    out = torch.empty_like(q).cuda()
+    sa.qk_norm_rope(rope, q.cuda(), None, dev_tensor(pos), out, None)
+    assert_rows(out, *want(q.float().numpy(), pos, 0))
+    x = bf16(rng, 2, 2, 128)
+    x[0, 0, 70] = float("inf")   # not rotated: the finite values become 0, the infinite one NaN
+    x[1, 0, 100] = float("nan")
+    out = torch.empty_like(x).cuda()
+    sa.qk_norm_rope(rope, x.cuda(), None, dev_tensor(pos[:2]), out, None)
+    o = out.cpu()
+    assert torch.isnan(o[0, 0, 70]) and (o[0, 0, 71:] == 0).all() and torch.isnan(o[1, 0]).all()
+    assert torch.isfinite(o[:, 1]).all()
+    # without norm an infinity stays in its pair, and what is not rotated passes bit for bit
+    rope, _ = make_rope(rng, rotary=64, norm=False)
+    x[0, 0, 3] = float("-inf")
+    sa.qk_norm_rope(rope, x.cuda(), None, dev_tensor(pos[:2]), out, None)
+    o = out.cpu()
+    assert not torch.isfinite(o[0, 0, [3, 35]]).any() and torch.isfinite(o[0, 0, [0, 1, 2, 4, 34, 36]]).all()
+    assert torch.equal(o[0, 0, 64:], x[0, 0, 64:]) and torch.isnan(o[1, 0, 100])
+
+
+# -------------------------------------------------------------------- appends
+def append_case(seed, seq_lens, q_lens, hq=8, hkv=2, spare=3):
+    rng = np.random.default_rng(seed)
+    seq_lens, q_lens = np.asarray(seq_lens, np.int32), np.asarray(q_lens, np.int32)
+    need = (np.maximum(seq_lens, 0) + 255) // 256
+    pages = int(need.sum()) + spare
+    free = rng.permutation(pages)
+    table = np.full((len(seq_lens), max(1, int(need.max()))), -1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = free[at:at + n]
+        at += n
+    total = int(q_lens.sum())
+    return rng, dict(seq_lens=seq_lens, q_lens=q_lens, table=table, pages=pages, total=total, hq=hq, hkv=hkv,
+                     qkv=bf16(rng, max(total, 1), hq + 2 * hkv, 128)[:total])
+
+
+def pools(rng, kind, pages, hkv):
+    shape = (pages, hkv, 256)
+    if kind == "bf16":
+        return [bf16(rng, *shape, 128) for _ in range(2)]
+    codes = [torch.from_numpy(rng.integers(-127, 128, (*shape, 128)).astype(np.int8)) if kind == "q8" else
+             torch.from_numpy(rng.integers(0, 256, (*shape, 64)).astype(np.uint8)) for _ in range(2)]
+    return codes + [torch.from_numpy(rng.random(shape).astype(np.float32)) for _ in range(2)]
+
+
+def call_append(kind, rope, c, pool, total=None, max_q=None, positions=None, with_q=True):
+    total = c["total"] if total is None else total
+    d = sa.dims_for(len(c["seq_lens"]), c["hq"], c["hkv"], c["pages"], c["table"].shape[1], total,
+                    int(max(1, c["q_lens"].max())) if max_q is None else max_q)
+    qkv = c["qkv"]
+    if total > qkv.shape[0]:
+        qkv = torch.cat([qkv, torch.ones(total - qkv.shape[0], *qkv.shape[1:], dtype=qkv.dtype)])
+    qkv = qkv.cuda()
+    hq, hkv = c["hq"], c["hkv"]
+    q_out = torch.full((total, hq, 128), 7.0, dtype=torch.bfloat16).cuda()
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    dev = [p.cuda() for p in pool]
+    fn = {"bf16": sa.kv_append_rope, "q8": sa.kv_append_rope_q8, "q4": sa.kv_append_rope_q4}[kind]
+    fn(d, rope, qkv[:, :hq] if with_q else None, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], q_out if with_q else None, *dev,
+       dev_tensor(c["table"]), dev_tensor(c["seq_lens"]), dev_tensor(c["q_lens"]),
+       positions=None if positions is None else dev_tensor(positions), err_flag=err)
+    torch.cuda.synchronize()
+    return q_out.cpu(), [p.cpu() for p in dev], int(err.item())
+
+
+def decoded(kind, pool):
+    """The values of a code pool and the largest |code|."""
+    if kind == "q8":
+        return pool.double().numpy()
+    n = pool.numpy().astype(np.int64)
+    return np.stack([(n & 15) - 8, (n >> 4) - 8], -1).reshape(*n.shape[:-1], 128).astype(np.float64)
+
+
+def check_append(kind, c, want, q_out, got, before, positions=None, skip=(), with_q=True):
+    """Every new row against its definition, everything else against before."""
+    hq, hkv = c["hq"], c["hkv"]
+    touched = np.zeros(got[0].shape[:3], bool)
+    row = 0
+    for b, (T, n) in enumerate(zip(c["seq_lens"], c["q_lens"])):
+        n = max(int(n), 0)
+        rows = np.arange(row, row + n)
+        row += n
+        if b in skip or n == 0:
+            continue
+        cache = np.arange(T - n, T)
+        pos = cache if positions is None else positions[rows]
+        x = c["qkv"][rows].float().numpy()
+        if with_q:
+            assert_rows(q_out[rows], *want(x[:, :hq], pos, 0), f"q of {b}")
+        page, slot = c["table"][b, cache // 256], cache % 256
+        touched[page, :, slot] = True
+        wk, size = want(x[:, hq:hq + hkv], pos, 1)
+        v_bits = c["qkv"][rows][:, hq + hkv:]
+        if kind == "bf16":
+            assert_rows(got[0][page, :, slot], wk, size, f"k of {b}")
+            assert torch.equal(got[1][page, :, slot].view(torch.int16), v_bits.view(torch.int16))
+            continue
+        top = 127 if kind == "q8" else 7
+        amax = np.abs(wk).max(-1)
+        step = got[2][page, :, slot].double().numpy()
+        # the scale's division is one rounding more
+        assert (np.abs(step - amax / top) <= (WORK * size.max(-1) + 2.0 ** -23 * amax) / top).all()
+        value = decoded(kind, got[0][page, :, slot]) * step[..., None]
+        assert (np.abs(value - wk) <= 0.5 * step[..., None] + WORK * (size + size.max(-1, keepdims=True))).all()
+        quant = oracle.quantize_q8 if kind == "q8" else oracle.quantize_q4
+        codes, scales = quant(v_bits.contiguous().view(torch.int16).numpy().view(np.uint16))
+        assert np.array_equal(got[1][page, :, slot].numpy(), codes) and np.array_equal(got[3][page, :, slot].numpy(), scales)
+    for g, p in zip(got, before):
+        a, b = g.numpy() if g.dtype != torch.bfloat16 else g.view(torch.int16).numpy(), p.numpy() if p.dtype != torch.bfloat16 else p.view(torch.int16).numpy()
+        assert np.array_equal(a[~touched], b[~touched])
+
+
+SHAPES = [([1], [1]), ([300, 1, 511, 256, 257], [1, 1, 1, 1, 1]), ([6, 700, 512, 40], [6, 6, 6, 6]), ([512, 600], [512, 300]),
+          ([260, 30, 900, 5, 3], [0, 3, 260, 0, 1]), (list(range(1, 301)), [1, 0, 2] + [1] * 297)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8", "q4"])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_append(kind, shape):
+    rng, c = append_case(40 + shape, *SHAPES[shape], hq=(8, 6, 32, 4, 10, 2)[shape], hkv=(2, 3, 8, 1, 5, 1)[shape])
+    rope, want = make_rope(rng, rotary=(128, 64, 128, 16, 96, 128)[shape], interleaved=shape in (1, 4), norm=shape != 2)
+    pool = pools(rng, kind, c["pages"], c["hkv"])
+    q_out, got, err = call_append(kind, rope, c, pool)
+    assert err == 0
+    check_append(kind, c, want, q_out, got, pool)
+
+
+def test_append_without_queries_at_given_positions():
+    rng, c = append_case(60, [300, 20], [5, 20])
+    rope, want = make_rope(rng)
+    pool = pools(rng, "bf16", c["pages"], c["hkv"])
+    positions = rng.integers(0, 100000, c["total"]).astype(np.int32)
+    _, got, err = call_append("bf16", rope, c, pool, positions=positions, with_q=False)
+    assert err == 0
+    check_append("bf16", c, want, None, got, pool, positions=positions, with_q=False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8", "q4"])
+def test_no_norm_and_no_rotation_is_kv_append(kind):
+    rng, c = append_case(61, [300, 20, 513], [5, 20, 1])
+    rope, _ = make_rope(rng, rotary=0, norm=False)
+    pool = pools(rng, kind, c["pages"], c["hkv"])
+    q_out, got, err = call_append(kind, rope, c, pool)
+    assert err == 0 and torch.equal(q_out, c["qkv"][:, :c["hq"]])
+    d = sa.dims_for(3, c["hq"], c["hkv"], c["pages"], c["table"].shape[1], c["total"], 20)
+    dev = [p.cuda() for p in pool]
+    plain = {"bf16": sa.kv_append, "q8": sa.kv_append_q8, "q4": sa.kv_append_q4}[kind]
+    k, v = (c["qkv"][:, a:a + c["hkv"]].contiguous().cuda() for a in (c["hq"], c["hq"] + c["hkv"]))
+    plain(d, k, v, *dev, dev_tensor(c["table"]), dev_tensor(c["seq_lens"]), dev_tensor(c["q_lens"]))
+    for a, b in zip(got, dev):
+        assert torch.equal(a, b.cpu())
+
+
+def test_rows_behind_the_last_sequence_stay():
+    rng, c = append_case(62, [300, 20], [5, 4])
+    rope, want = make_rope(rng)
+    pool = pools(rng, "bf16", c["pages"], c["hkv"])
+    q_out, got, err = call_append("bf16", rope, c, pool, total=c["total"] + 3)
+    assert err == 0 and (q_out[c["total"]:] == 7).all()
+    check_append("bf16", c, want, q_out, got, pool)
+
+
+@pytest.mark.parametrize("bad", ["len", "max", "negative", "total"])
+def test_inconsistent_sequences_are_flagged_and_skipped(bad):
+    rng, c = append_case(63, [300, 20, 400], [5, 4, 6])
+    rope, want = make_rope(rng)
+    pool = pools(rng, "bf16", c["pages"], c["hkv"])
+    max_q, total, skip = 6, c["total"], {1}
+    if bad == "len":
+        c["seq_lens"][1] = 3
+    elif bad == "max":
+        max_q, skip = 5, {2}
+    elif bad == "negative":
+        c["q_lens"][1] = -4
+        c["qkv"] = torch.cat([c["qkv"][:5], c["qkv"][9:]])
+        total = 11
+    else:
+        total, skip = c["total"] - 2, {2}
+    q_out, got, err = call_append("bf16", rope, {**c, "qkv": c["qkv"][:total]}, pool, total=total, max_q=max_q)
+    assert err == 1 << 7
+    check_append("bf16", c, want, q_out, got, pool, skip=skip)
+
+
+def test_page_out_of_range_is_flagged_and_skipped():
+    rng, c = append_case(64, [300, 20], [60, 4])
+    rope, want = make_rope(rng)
+    pool = pools(rng, "q8", c["pages"], c["hkv"])
+    for value in (-1, c["pages"]):
+        table = c["table"].copy()
+        c["table"][0, 1] = value            # tokens 256 .. 299 of sequence 0
+        q_out, got, err = call_append("q8", rope, c, pool)
+        c["table"][:] = table
+        assert err == 1 << 3
+        assert_rows(q_out[:60], *want(c["qkv"][:60, :8].float().numpy(), np.arange(240, 300), 0))
+        page = table[0, 1]
+        assert all(torch.equal(g[page], p[page]) for g, p in zip(got, pool))
+
+
+def test_binding_refuses_wrong_tensors():
+    rng, c = append_case(65, [30, 20], [2, 4])
+    rope, _ = make_rope(rng)
+    pool = [p.cuda() for p in pools(rng, "bf16", c["pages"], 2)]
+    d = sa.dims_for(2, 8, 2, c["pages"], 1, 6, 4)
+    qkv = c["qkv"].cuda()
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    bt, sl, ql = dev_tensor(c["table"]), dev_tensor(c["seq_lens"]), dev_tensor(c["q_lens"])
+    out = torch.zeros(6, 8, 128, dtype=torch.bfloat16, device="cuda")
+    good = dict(q=q, k_new=k, v_new=v, q_out=out, k_pages=pool[0], v_pages=pool[1], block_table=bt, seq_lens=sl, q_lens=ql)
+    for change in (dict(q=q.float()), dict(q=q[:5]), dict(q=q.cpu()), dict(q_out=out[:, :4]), dict(k_new=k.transpose(1, 2)),
+                   dict(v_new=None), dict(k_new=qkv[:, 8:12:2]), dict(k_pages=pool[0][1:]), dict(block_table=bt.long()),
+                   dict(seq_lens=sl[:1]), dict(q_lens=ql.cpu()), dict(q=None)):
+        with pytest.raises(ValueError):
+            sa.kv_append_rope(d, rope, **{**good, **change})
+    with pytest.raises(sa.SpecAttnError):   # token stride not a multiple of 16 bytes
+        wide = torch.zeros(6, 8 * 128 + 4, dtype=torch.bfloat16, device="cuda")
+        sa.kv_append_rope(d, rope, **{**good, "q": wide[:, :1024].unflatten(1, (8, 128))})
+    pos = torch.zeros(6, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        sa.qk_norm_rope(rope, q, k, pos, out, None)
+    with pytest.raises(ValueError):
+        sa.qk_norm_rope(rope, q, None, pos[:5], out, None)
+
+
+def test_on_another_stream_and_in_a_graph():
+    rng, c = append_case(66, [300, 20], [1, 1])
+    rope, want = make_rope(rng)
+    pool = pools(rng, "bf16", c["pages"], c["hkv"])
+    dev = [p.cuda() for p in pool]
+    d = sa.dims_for(2, 8, 2, c["pages"], 2, 2, 1)
+    qkv = c["qkv"].cuda()
+    bt, sl, ql = dev_tensor(c["table"]), dev_tensor(c["seq_lens"]), dev_tensor(c["q_lens"])
+    out = torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+    args = (d, rope, qkv[:, :8], qkv[:, 8:10], qkv[:, 10:], out, *dev, bt, sl, ql)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sa.kv_append_rope(*args, stream=side)
+    torch.cuda.synchronize()
+    check_append("bf16", c, want, out.cpu(), [p.cpu() for p in dev], pool)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.kv_append_rope(*args)
+    for p, q in zip(dev, pool):
+        p.copy_(q)
+    sl += 1                                     # the lengths are read at replay
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    c["seq_lens"] = c["seq_lens"] + 1
+    check_append("bf16", c, want, out.cpu(), [p.cpu() for p in dev], pool)
