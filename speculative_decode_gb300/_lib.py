@@ -124,10 +124,25 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream_getter():
+    """The address of torch's current stream: its raw getter, where torch has one,
+    makes no Stream object (0.2 us of host time a call instead of 2.9)."""
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
+_current_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _current_stream_getter()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -334,7 +349,8 @@ def defrag_apply_bytes(num_pages: int, page_bytes: int, pool_a, pool_b, moves, n
 
 
 class _Types:
-    """torch dtypes by what the C ABI calls them (torch is imported with the first call that needs it)."""
+    """torch dtypes by what the C ABI calls them, and the device that is current
+    (torch is imported with the first call that needs it)."""
 
     def __init__(self):
         import torch
@@ -343,7 +359,9 @@ class _Types:
         self.i32 = (torch.int32,)
         self.i8 = (torch.int8,)
         self.u8 = (torch.uint8,)
-        self.current_device = torch.cuda.current_device
+        # no device: no tensor is on it, and every call refuses its tensors
+        self.here = (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device) if torch.cuda.is_available() \
+            else lambda: -2
 
 
 _types_made = None
@@ -356,40 +374,39 @@ def _types() -> _Types:
     return _types_made
 
 
-def _tensor(t, name: str, dtypes, shape=None, optional=False):
-    """Address of a packed CUDA tensor of one of these dtypes (and of that shape)."""
+def _refuse(t, name: str, dtypes, here: int, shape=None) -> None:
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
-    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtypes[0]} is wanted, got {t.dtype}, strides "
-                         f"{t.stride()}, on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name}: a CUDA tensor of {dtypes[0]} is wanted, got {t.dtype} on {t.device}")
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}" +
+                     (f", wanted {tuple(shape)}" if shape is not None else "") + ", packed")
+
+
+def _tensor(t, name: str, dtypes, here: int, shape=None) -> int:
+    """Address of a packed tensor of one of these dtypes (and of that shape) on the current device."""
+    if (t is None or t.get_device() != here or t.dtype not in dtypes or not t.is_contiguous() or
+            (shape is not None and t.shape != shape)):
+        _refuse(t, name, dtypes, here, shape)
     return t.data_ptr()
 
 
-def _heads(t, name: str, tokens: int, heads: int):
+def _heads(t, name: str, tokens: int, heads: int, here: int):
     """(address, token stride) of bf16 rows [tokens, heads, 128] whose heads are packed in their token."""
-    if t is None:
-        raise ValueError(f"{name} is missing")
-    if not t.is_cuda or t.dtype not in _types().bf16:
-        raise ValueError(f"{name}: a CUDA tensor of bf16 values is wanted, got {t.dtype} on {t.device}")
-    if t.shape != (tokens, heads, 128):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {(tokens, heads, 128)}")
+    bf16 = _types_made.bf16
+    if t is None or t.get_device() != here or t.dtype not in bf16 or t.shape != (tokens, heads, 128):
+        _refuse(t, name, bf16, here, (tokens, heads, 128))
     step, head, value = t.stride()
     if tokens and (value != 1 or (head != 128 and heads > 1)):
-        raise ValueError(f"{name}: a token's heads and their values must be packed, strides {t.stride()}")
+        _refuse(t, name, bf16, here, (tokens, heads, 128))
     return t.data_ptr(), (step if tokens > 1 else heads * 128)
 
 
-def _same_device(*tensors) -> None:
-    """The tensors of a call are on the device that is current: its context takes the launch."""
-    here = _types().current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+def _here() -> int:
+    """The current device: its context takes the launch, so a call's tensors have to be on it."""
+    return (_types_made or _types()).here()
 
 
 class Rope:
@@ -399,14 +416,23 @@ class Rope:
 
     def __init__(self, inv_freq=None, rotary_dim=128, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
         f32 = _types().f32
-        self._struct = _RopeStruct(
-            _tensor(inv_freq, "inv_freq", f32, (rotary_dim // 2,), optional=rotary_dim == 0),
-            _tensor(q_weight, "q_weight", f32, (128,), optional=True),
-            _tensor(k_weight, "k_weight", f32, (128,), optional=True),
-            eps, rotary_dim, 1 if interleaved else 0)
+        tensors = [(inv_freq, "inv_freq", (rotary_dim // 2,)), (q_weight, "q_weight", (128,)), (k_weight, "k_weight", (128,))]
+        if inv_freq is None and rotary_dim:
+            raise ValueError("inv_freq is missing")
+        for t, name, _ in tensors:
+            if t is not None and not t.is_cuda:
+                raise ValueError(f"{name}: a CUDA tensor is wanted, got one on {t.device}")
+        here = self._device = _here() if any(t is not None for t, _, _ in tensors) else None
+        self._struct = _RopeStruct(*[None if t is None else _tensor(t, name, f32, here, shape) for t, name, shape in tensors],
+                                   eps, rotary_dim, 1 if interleaved else 0)
         self._kept = (inv_freq, q_weight, k_weight)
-        _same_device(*self._kept)
         self._ref = ctypes.byref(self._struct)
+
+    def _on(self, here: int):
+        """The struct, for a call on this device."""
+        if self._device is not None and self._device != here:
+            raise ValueError(f"the Rope's tensors are on cuda:{self._device}, the current device is cuda:{here}")
+        return self._ref
 
 
 def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None:
@@ -415,41 +441,47 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
     values); q with q_out, or k with k_out, may be None."""
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
         raise ValueError("q with q_out, k with k_out, or both are wanted")
+    here = _here()
     n = (k if q is None else q).shape[0]
-    hq = 0 if q is None else q.shape[1]
-    hk = 0 if k is None else k.shape[1]
-    qp, qs = (None, 0) if q is None else _heads(q, "q", n, hq)
-    qo, qos = (None, 0) if q is None else _heads(q_out, "q_out", n, hq)
-    kp, ks = (None, 0) if k is None else _heads(k, "k", n, hk)
-    ko, kos = (None, 0) if k is None else _heads(k_out, "k_out", n, hk)
-    pos = _tensor(positions, "positions", _types().i32, (n,))
-    _same_device(q, k, positions, q_out, k_out, *rope._kept)
-    _check(load_library().sa_qk_norm_rope(rope._ref, n, hq, hk, 128, qp, qs, kp, ks, pos, qo, qos, ko, kos,
-                                          _stream(stream)), "sa_qk_norm_rope")
+    hq = hk = qs = qos = ks = kos = 0
+    qp = qo = kp = ko = None
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _heads(q, "q", n, hq, here)
+        qo, qos = _heads(q_out, "q_out", n, hq, here)
+    if k is not None:
+        hk = k.shape[1]
+        kp, ks = _heads(k, "k", n, hk, here)
+        ko, kos = _heads(k_out, "k_out", n, hk, here)
+    pos = _tensor(positions, "positions", _types_made.i32, here, (n,))
+    rc = load_library().sa_qk_norm_rope(rope._on(here), n, hq, hk, 128, qp, qs, kp, ks, pos, qo, qos, ko, kos,
+                                        _stream(stream))
+    if rc:
+        _check(rc, "sa_qk_norm_rope")
 
 
 def _append_rope(name, dims, rope, q, k_new, v_new, q_out, pools, pool_types, block_table, seq_lens, q_lens,
                  positions, err_flag, stream) -> None:
+    here, i32 = _here(), _types_made.i32
     n, hkv, pages, B = dims.total_q, dims.num_kv_heads, dims.num_pages, dims.num_seqs
-    types = _types()
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
     qp, qs, qo = None, 0, None
-    if q is not None:
-        qp, qs = _heads(q, "q", n, dims.num_q_heads)
-        qo = _tensor(q_out, "q_out", types.bf16, (n, dims.num_q_heads, 128))
-    kp, ks = _heads(k_new, "k_new", n, hkv)
-    vp, vs = _heads(v_new, "v_new", n, hkv)
-    addresses = [_tensor(t, "page pool", dt, (pages, hkv, 256, row) if row else (pages, hkv, 256))
+    if q is not None or q_out is not None:
+        hq = dims.num_q_heads
+        qp, qs = _heads(q, "q", n, hq, here)
+        qo = _tensor(q_out, "q_out", _types_made.bf16, here, (n, hq, 128))
+    kp, ks = _heads(k_new, "k_new", n, hkv, here)
+    vp, vs = _heads(v_new, "v_new", n, hkv, here)
+    addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
                  for t, (dt, row) in zip(pools, pool_types)]
-    bt = _tensor(block_table, "block_table", types.i32, (B, dims.max_pages_per_seq))
-    sl = _tensor(seq_lens, "seq_lens", types.i32, (B,))
-    ql = _tensor(q_lens, "q_lens", types.i32, (B,))
-    ps = _tensor(positions, "positions", types.i32, (n,), optional=True)
-    err = _tensor(err_flag, "err_flag", types.i32, optional=True)
-    _same_device(q, q_out, k_new, v_new, *pools, block_table, seq_lens, q_lens, positions, err_flag, *rope._kept)
-    _check(getattr(load_library(), name)(ctypes.byref(dims), rope._ref, qp, qs, kp, ks, vp, vs, qo, *addresses, bt, sl,
-                                         ql, ps, err, _stream(stream)), name)
+    bt = _tensor(block_table, "block_table", i32, here, (B, dims.max_pages_per_seq))
+    sl = _tensor(seq_lens, "seq_lens", i32, here, (B,))
+    ql = _tensor(q_lens, "q_lens", i32, here, (B,))
+    ps = None if positions is None else _tensor(positions, "positions", i32, here, (n,))
+    err = None if err_flag is None else _tensor(err_flag, "err_flag", i32, here)
+    rc = getattr(load_library(), name)(ctypes.byref(dims), rope._on(here), qp, qs, kp, ks, vp, vs, qo, *addresses, bt, sl,
+                                       ql, ps, err, _stream(stream))
+    if rc:
+        _check(rc, name)
 
 
 def kv_append_rope(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, q_lens,
@@ -490,52 +522,52 @@ def beam_select(logits, scores, tokens, parents, scores_out, workspace, finished
     continuations of every group. logits [groups, beams, vocab] may be a view
     whose rows are evenly spaced (a padded vocabulary); scores and finished
     [groups, beams]; the outputs [groups, picks]."""
-    types = _types()
+    here, types = _here(), _types_made
     wide = logits.dtype in types.f32
-    if logits.dim() != 3 or not logits.is_cuda or not (wide or logits.dtype in types.bf16):
-        raise ValueError(f"logits: fp32 or bf16 values [groups, beams, vocab] on a GPU are wanted, got {logits.dtype} "
-                         f"{tuple(logits.shape)} on {logits.device}")
+    if logits.dim() != 3 or logits.get_device() != here or not (wide or logits.dtype in types.bf16):
+        raise ValueError(f"logits: fp32 or bf16 values [groups, beams, vocab] on cuda:{here} are wanted, got "
+                         f"{logits.dtype} {tuple(logits.shape)} on {logits.device}")
     B, W, V = logits.shape
     group, row, value = logits.stride()
     if W == 1:
-        row = group if B > 1 else V
+        row = group
     if (V > 1 and value != 1) or (B > 1 and group != W * row):
         raise ValueError(f"logits: packed values and evenly spaced rows are wanted, strides {logits.stride()}")
     if B * W <= 1:
         row = V
     K = tokens.shape[-1]
-    picks, beams = (B, K), (B, W)
-    sc = _tensor(scores, "scores", types.f32, beams)
-    fi = _tensor(finished, "finished", types.i32, beams, optional=True)
-    to = _tensor(tokens, "tokens", types.i32, picks)
-    pa = _tensor(parents, "parents", types.i32, picks)
-    so = _tensor(scores_out, "scores_out", types.f32, picks)
-    fo = _tensor(finished_out, "finished_out", types.i32, picks, optional=True)
-    ws = _tensor(workspace, "workspace", types.u8)
-    _same_device(logits, scores, tokens, parents, scores_out, workspace, finished, finished_out)
+    picks, beams, i32, f32 = (B, K), (B, W), types.i32, types.f32
+    sc = _tensor(scores, "scores", f32, here, beams)
+    fi = None if finished is None else _tensor(finished, "finished", i32, here, beams)
+    to = _tensor(tokens, "tokens", i32, here, picks)
+    pa = _tensor(parents, "parents", i32, here, picks)
+    so = _tensor(scores_out, "scores_out", f32, here, picks)
+    fo = None if finished_out is None else _tensor(finished_out, "finished_out", i32, here, picks)
+    ws = _tensor(workspace, "workspace", types.u8, here)
     lib = load_library()
-    call = lib.sa_beam_select if wide else lib.sa_beam_select_bf16
-    _check(call(logits.data_ptr(), row, sc, fi, B, W, V, K, eos_token, to, pa, so, fo, ws, workspace.numel(),
-                _stream(stream)), "sa_beam_select")
+    rc = (lib.sa_beam_select if wide else lib.sa_beam_select_bf16)(
+        logits.data_ptr(), row, sc, fi, B, W, V, K, eos_token, to, pa, so, fo, ws, workspace.numel(), _stream(stream))
+    if rc:
+        _check(rc, "sa_beam_select" if wide else "sa_beam_select_bf16")
 
 
 def _beam_reorder(name, dims, beam_width, parents, block_table, seq_lens, block_table_out, pools, pool_types, err_flag,
                   stream) -> None:
-    types = _types()
+    here, i32 = _here(), _types_made.i32
     B, hkv, pages = dims.num_seqs, dims.num_kv_heads, dims.num_pages
     table = (B, dims.max_pages_per_seq)
-    addresses = [_tensor(t, "page pool", dt, (pages, hkv, 256, row) if row else (pages, hkv, 256))
+    addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
                  for t, (dt, row) in zip(pools, pool_types)]
-    pa = _tensor(parents, "parents", types.i32)
+    pa = _tensor(parents, "parents", i32, here)
     if parents.numel() != B:
         raise ValueError(f"parents: {parents.numel()} values for {B} sequences")
-    bt = _tensor(block_table, "block_table", types.i32, table)
-    sl = _tensor(seq_lens, "seq_lens", types.i32, (B,))
-    bo = _tensor(block_table_out, "block_table_out", types.i32, table)
-    err = _tensor(err_flag, "err_flag", types.i32, optional=True)
-    _same_device(parents, block_table, seq_lens, block_table_out, *pools, err_flag)
-    _check(getattr(load_library(), name)(ctypes.byref(dims), beam_width, pa, bt, sl, bo, *addresses, err,
-                                         _stream(stream)), name)
+    bt = _tensor(block_table, "block_table", i32, here, table)
+    sl = _tensor(seq_lens, "seq_lens", i32, here, (B,))
+    bo = _tensor(block_table_out, "block_table_out", i32, here, table)
+    err = None if err_flag is None else _tensor(err_flag, "err_flag", i32, here)
+    rc = getattr(load_library(), name)(ctypes.byref(dims), beam_width, pa, bt, sl, bo, *addresses, err, _stream(stream))
+    if rc:
+        _check(rc, name)
 
 
 def beam_reorder(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_pages, v_pages,

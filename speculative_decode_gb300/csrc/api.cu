@@ -729,8 +729,11 @@ int sa_qk_norm_rope(const sa_rope *rope, int32_t num_tokens, int32_t num_q_heads
     p.positions = positions;
     p.Hq = num_q_heads;
     p.Hkv = num_kv_heads;
+    p.total_q = num_tokens;
+    const int sms = device_sm_count();
+    if (sms <= 0) return SA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_rope(p, 0, num_tokens, s) != cudaSuccess) return SA_ERR_CUDA;
+    if (launch_rope(p, 0, sms, s) != cudaSuccess) return SA_ERR_CUDA;
     return finish(s, nullptr);
 }
 
@@ -761,8 +764,10 @@ static int append_rope(const sa_dims *dims, const sa_rope *rope, RopeParams &p, 
     p.max_pages = d.max_pages_per_seq;
     p.max_q_len = d.max_q_len;
     p.total_q = d.total_q;
+    const int sms = device_sm_count();
+    if (sms <= 0) return SA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_rope(p, bits, d.total_q, s) != cudaSuccess) return SA_ERR_CUDA;
+    if (launch_rope(p, bits, sms, s) != cudaSuccess) return SA_ERR_CUDA;
     return finish(s, p.err);
 }
 

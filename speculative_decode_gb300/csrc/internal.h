@@ -181,9 +181,10 @@ struct RopeParams {
     float eps;
     int32_t half, interleaved;    // pairs, and whether they are neighbours
     int32_t B, Hq, Hkv, num_pages, max_pages, max_q_len, total_q;
+    int32_t parts_log2;           // warps a token (set at launch)
 };
 // code_bits 0: dense keys; 16, 8, 4: pages of that kind
-cudaError_t launch_rope(const RopeParams &p, int code_bits, int num_tokens, cudaStream_t stream);
+cudaError_t launch_rope(RopeParams p, int code_bits, int sms, cudaStream_t stream);
 
 // Beam search (beam.cu).
 constexpr int kMaxBeamWidth = 32;

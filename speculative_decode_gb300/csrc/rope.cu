@@ -10,10 +10,12 @@
 // int4 page rows). t is formed in 64 bits, as a fraction of a turn: at
 // position 10^6 a 32-bit product would be off by up to 0.06 rad.
 //
-// Half a warp holds a row, 16 bytes a lane; a CTA takes one token, whose
-// angles its first threads compute once for all heads. Bound: bytes moved (a
-// row in, a row out) for many tokens, two dependent memory round trips
-// (lengths, then rows) for few.
+// Half a warp holds a row, 16 bytes a lane. A warp takes one token, or every
+// `parts`-th pair of a token's rows where there are few tokens: its lanes
+// compute the token's angles once for all its rows, and no warp waits for
+// another after the token's sequence is found. Bound: bytes moved (a row in, a row
+// out) for many tokens, two dependent memory round trips (lengths, then rows)
+// for few.
 #include <cfloat>
 
 #include "common.cuh"
@@ -22,9 +24,9 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;  // rows in one step of a CTA
-constexpr int kUnroll = 3;              // rows in flight per lane
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kFlight = 4;  // row pairs in flight per warp
 
 __device__ __forceinline__ float half_warp_sum(float v, uint32_t mask) {
 #pragma unroll
@@ -41,7 +43,7 @@ __device__ __forceinline__ float half_warp_max(float v, uint32_t mask) {
 // y = x * rsqrt(mean(x^2) + eps) * w for the half warp's row. A sum of squares
 // past 32 bits is formed again of scaled values (a power of two), so rows of
 // any finite values have their norm.
-__device__ __forceinline__ void norm_row(float (&y)[8], const float *w, float eps, int l, uint32_t mask) {
+__device__ __forceinline__ void norm_row(float (&y)[8], const float (&w)[8], float eps, uint32_t mask) {
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
@@ -58,16 +60,8 @@ __device__ __forceinline__ void norm_row(float (&y)[8], const float *w, float ep
         s2 = half_warp_sum(s2, mask);
         r = rsqrtf(s2 * (1.f / kHeadDim));  // eps is far below such a row's mean
     }
-    const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l));
-    const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l) + 1);
-    y[0] *= r * w0.x;
-    y[1] *= r * w0.y;
-    y[2] *= r * w0.z;
-    y[3] *= r * w0.w;
-    y[4] *= r * w1.x;
-    y[5] *= r * w1.y;
-    y[6] *= r * w1.z;
-    y[7] *= r * w1.w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
 }
 
 // The page format of the quantising appends (see kv_append.cu), half a warp a
@@ -99,13 +93,13 @@ struct TokenPlace {
     int first;  // the sequence's first packed row
 };
 
-// The sequence that owns a packed row, from all sequences' query counts: each
-// thread sums a run of them, a block-wide scan gives the runs' starts, and the
-// thread whose run holds the row walks it. seq is -1 behind the last row. CTA 0
-// also checks every sequence (each other CTA skips the rows of a bad one).
-__device__ __forceinline__ TokenPlace locate(const RopeParams &P, int token) {
-    __shared__ long long s_total[kThreads / 32];
-    __shared__ TokenPlace s_place;
+// The sequences that own the packed rows [token, token + kWarps), from all
+// sequences' query counts: each thread sums a run of them, a block-wide scan
+// gives the runs' starts, and the threads whose runs hold the rows walk them.
+// seq is -1 behind the last row. Block 0 also checks every sequence (each block
+// skips the rows of a bad one).
+__device__ __forceinline__ void locate(const RopeParams &P, int token, TokenPlace (&place)[kWarps]) {
+    __shared__ long long s_total[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (P.B + kThreads - 1) / kThreads;
     const int lo = min(P.B, static_cast<int>(threadIdx.x) * per), hi = min(P.B, lo + per);
@@ -119,7 +113,7 @@ __device__ __forceinline__ TokenPlace locate(const RopeParams &P, int token) {
         if (lane >= o) incl += up;
     }
     if (lane == 31) s_total[warp] = incl;
-    if (threadIdx.x == 0) s_place.seq = -1;
+    if (threadIdx.x < kWarps) place[threadIdx.x].seq = -1;
     __syncthreads();
     long long at = incl - sum;
     for (int w = 0; w < warp; ++w) at += s_total[w];
@@ -133,33 +127,45 @@ __device__ __forceinline__ TokenPlace locate(const RopeParams &P, int token) {
         }
         if (bad) flag_error(P.err, kErrBitQlen);
     }
-    if (token >= at && token < at + sum) {
-        int b = lo;
-        while (token >= at + max(P.q_lens[b], 0)) at += max(P.q_lens[b++], 0);
-        s_place = TokenPlace{b, P.q_lens[b], b == lo ? len0 : P.seq_lens[b], static_cast<int>(at)};
+    if (at < token + kWarps && at + sum > token) {
+        for (int b = lo; b < hi && at < token + kWarps; ++b) {
+            const int n = max(P.q_lens[b], 0);
+            for (int k = 0; k < kWarps; ++k)
+                if (token + k >= at && token + k < at + n)
+                    place[k] = TokenPlace{b, n, b == lo ? len0 : P.seq_lens[b], static_cast<int>(at)};
+            at += n;
+        }
     }
     __syncthreads();
-    return s_place;
 }
 
 // KB: 0 for dense keys (no pages), 16 for bf16 pages, 8 or 4 for code pages.
 template <int KB>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams P) {
-    __shared__ __align__(16) float s_cos[kHeadDim / 2], s_sin[kHeadDim / 2];
+    __shared__ __align__(16) float s_cos[kWarps][kHeadDim / 2], s_sin[kWarps][kHeadDim / 2];
     // the attention kernel that follows reads q and the pages only after this
     // grid has completed
     if constexpr (KB != 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int token = blockIdx.x;
-    const int l = threadIdx.x & 15;
-    const int group = threadIdx.x >> 4;
-    const uint32_t mask = 0xffffu << (threadIdx.x & 16);
-    const float freq = threadIdx.x < P.half ? P.inv_freq[threadIdx.x] : 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane & 15, side = lane >> 4;
+    const uint32_t mask = 0xffffu << (lane & 16);
+    const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int token = static_cast<int>(gw >> P.parts_log2);
+    const int part = static_cast<int>(gw) & ((1 << P.parts_log2) - 1);
+    // two angles a lane
+    const float freq0 = lane < P.half ? P.inv_freq[lane] : 0.f;
+    const float freq1 = lane + 32 < P.half ? P.inv_freq[lane + 32] : 0.f;
 
     int pos, pid = 0, slot = 0;
     if constexpr (KB == 0) {
+        if (token >= P.total_q) return;
         pos = P.positions[token];
     } else {
-        const TokenPlace at = locate(P, token);
+        __shared__ TokenPlace s_place[kWarps];
+        const int token0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * kWarps >> P.parts_log2);
+        locate(P, token0, s_place);
+        if (token >= P.total_q) return;
+        const TokenPlace at = s_place[token - token0];
         if (at.seq < 0 || at.n > at.len || at.n > P.max_q_len || at.first + static_cast<long long>(at.n) > P.total_q)
             return;
         pos = at.len - at.n + (token - at.first);
@@ -169,87 +175,108 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams P) {
         if (P.positions != nullptr) pos = P.positions[token];
     }
 
-    const int rows = P.Hq + (KB == 0 ? P.Hkv : 2 * P.Hkv);
-    bool turned = false;  // the angles are in shared memory
-    float c[8], s[8];
+    // pairs of rows: the queries', the keys', then the values'
+    const int nq = (P.Hq + 1) / 2, nk = (P.Hkv + 1) / 2;
+    const int pairs = nq + (KB == 0 ? nk : 2 * nk);
+    const int parts = 1 << P.parts_log2;
+    const uint16_t *q = P.q + token * P.q_stride + 8 * l;
+    const uint16_t *k = P.k + token * P.k_stride + 8 * l;
+    const uint16_t *v = P.v + token * P.v_stride + 8 * l;
+    bool turned = false;  // the angles are there
+    float c[8], s[8], w[8];
+    int w_of = -1;        // whose weights w holds: 0 queries, 1 keys
     const int sh = P.half / 8;
     const bool rot = l < 2 * sh;
-    for (int r0 = group; r0 - group < rows; r0 += kGroups * kUnroll) {
-        uint4 raw[kUnroll];
+    const int other = !rot || P.interleaved ? l : l < sh ? l + sh : l - sh;
+    for (int p0 = part; p0 < pairs; p0 += parts * kFlight) {
+        uint4 raw[kFlight];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = r0 + u * kGroups;
-            const uint16_t *src = r < P.Hq          ? P.q + token * P.q_stride + r * kHeadDim
-                                  : r < P.Hq + P.Hkv ? P.k + token * P.k_stride + (r - P.Hq) * kHeadDim
-                                                     : P.v + token * P.v_stride + (r - P.Hq - P.Hkv) * kHeadDim;
-            raw[u] = r < rows ? *reinterpret_cast<const uint4 *>(src + 8 * l) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < kFlight; ++u) {
+            const int p = p0 + u * parts;
+            const int kind = p < nq ? 0 : p < nq + nk ? 1 : 2;
+            const int head = 2 * (p - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + side;
+            const uint16_t *src = (kind == 0 ? q : kind == 1 ? k : v) + head * kHeadDim;
+            raw[u] = p < pairs && head < (kind == 0 ? P.Hq : P.Hkv) ? *reinterpret_cast<const uint4 *>(src)
+                                                                   : make_uint4(0, 0, 0, 0);
         }
         if (!turned) {  // while the first rows are on their way
-            if (threadIdx.x < P.half) {
-                const double turns = static_cast<double>(pos) * (static_cast<double>(freq) * 0.15915494309189535);
-                const float part = static_cast<float>(2.0 * (turns - rint(turns)));
-                sincospif(part, &s_sin[threadIdx.x], &s_cos[threadIdx.x]);
-            }
-            __syncthreads();
+            const double to_turns = 0.15915494309189535;
+            auto turn = [&](float freq, int j) {
+                const double turns = static_cast<double>(pos) * (static_cast<double>(freq) * to_turns);
+                sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s_sin[warp][j], &s_cos[warp][j]);
+            };
+            if (lane < P.half) turn(freq0, lane);
+            if (lane + 32 < P.half) turn(freq1, lane + 32);
+            __syncwarp();
             turned = true;
             if (rot) {
                 const int j = P.interleaved ? 4 * l : 8 * (l < sh ? l : l - sh);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int je = P.interleaved ? j + e / 2 : j + e;
-                    c[e] = s_cos[je];
                     const bool second = P.interleaved ? (e & 1) : l >= sh;
-                    s[e] = second ? s_sin[je] : -s_sin[je];
+                    c[e] = s_cos[warp][je];
+                    s[e] = second ? s_sin[warp][je] : -s_sin[warp][je];
                 }
             }
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = r0 + u * kGroups;
-            if (r >= rows) continue;  // a whole half warp
-            const bool is_q = r < P.Hq, is_v = r >= P.Hq + P.Hkv;
+        for (int u = 0; u < kFlight; ++u) {
+            const int p = p0 + u * parts;
+            if (p >= pairs) break;
+            const int kind = p < nq ? 0 : p < nq + nk ? 1 : 2;
+            const int head = 2 * (p - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + side;
+            const bool here = head < (kind == 0 ? P.Hq : P.Hkv);  // a whole half warp
             float y[8] = {bf16_lo(raw[u].x), bf16_hi(raw[u].x), bf16_lo(raw[u].y), bf16_hi(raw[u].y),
                           bf16_lo(raw[u].z), bf16_hi(raw[u].z), bf16_lo(raw[u].w), bf16_hi(raw[u].w)};
             uint4 packed = raw[u];
-            if (!is_v) {
-                const float *w = is_q ? P.q_weight : P.k_weight;
-                if (w != nullptr) norm_row(y, w, P.eps, l, mask);
-                float p[8];
+            if (kind != 2) {
+                const float *weight = kind == 0 ? P.q_weight : P.k_weight;
+                if (weight != nullptr) {
+                    if (w_of != kind) {
+                        const float4 a = __ldg(reinterpret_cast<const float4 *>(weight + 8 * l));
+                        const float4 b = __ldg(reinterpret_cast<const float4 *>(weight + 8 * l) + 1);
+                        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+                        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+                        w_of = kind;
+                    }
+                    norm_row(y, w, P.eps, mask);
+                }
+                float o[8];
                 if (P.interleaved) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
+                    for (int e = 0; e < 8; ++e) o[e] = y[e ^ 1];
                 } else {
-                    const int other = !rot ? l : l < sh ? l + sh : l - sh;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(mask, y[e], other, 16);
+                    for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(mask, y[e], other, 16);
                 }
                 if (rot) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], c[e], p[e] * s[e]);
+                    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], c[e], o[e] * s[e]);
                 }
                 packed = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                                     pack_bf16x2(y[6], y[7]));
             }
-            if (is_q) {
-                *reinterpret_cast<uint4 *>(P.q_out + token * P.q_out_stride + r * kHeadDim + 8 * l) = packed;
+            if (!here) continue;
+            if (kind == 0) {
+                *reinterpret_cast<uint4 *>(P.q_out + token * P.q_out_stride + head * kHeadDim + 8 * l) = packed;
                 continue;
             }
             if constexpr (KB == 0) {
-                *reinterpret_cast<uint4 *>(P.k_out + token * P.k_out_stride + (r - P.Hq) * kHeadDim + 8 * l) = packed;
+                *reinterpret_cast<uint4 *>(P.k_out + token * P.k_out_stride + head * kHeadDim + 8 * l) = packed;
             } else {
                 if (pid < 0 || pid >= P.num_pages) {
                     if (l == 0) flag_error(P.err, kErrBitPageOOB);
                     continue;
                 }
-                const int g = is_v ? r - P.Hq - P.Hkv : r - P.Hq;
-                const int64_t prow = (static_cast<int64_t>(pid) * P.Hkv + g) * kPageSize + slot;
+                const int64_t prow = (static_cast<int64_t>(pid) * P.Hkv + head) * kPageSize + slot;
                 if constexpr (KB == 16) {
-                    uint16_t *pages = is_v ? P.v_pages : P.k_pages;
+                    uint16_t *pages = kind == 2 ? P.v_pages : P.k_pages;
                     *reinterpret_cast<uint4 *>(pages + prow * kHeadDim + 8 * l) = packed;
                 } else {
                     constexpr int kCodeRow = kHeadDim * KB / 8;
-                    store_codes<KB>(y, l, mask, (is_v ? P.v_codes : P.k_codes) + prow * kCodeRow,
-                                    (is_v ? P.v_scales : P.k_scales) + prow);
+                    store_codes<KB>(y, l, mask, (kind == 2 ? P.v_codes : P.k_codes) + prow * kCodeRow,
+                                    (kind == 2 ? P.v_scales : P.k_scales) + prow);
                 }
             }
         }
@@ -258,12 +285,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams P) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams &p, int code_bits, int num_tokens, cudaStream_t stream) {
+cudaError_t launch_rope(RopeParams p, int code_bits, int sms, cudaStream_t stream) {
+    // a warp a token, and up to eight where that leaves SMs with few warps
+    int log2 = 0;
+    while (log2 < 3 && (static_cast<int64_t>(p.total_q) << log2) < 12ll * sms) ++log2;
+    p.parts_log2 = log2;
+    const int64_t warps = static_cast<int64_t>(p.total_q) << log2;
     auto kernel = code_bits == 0    ? rope_kernel<0>
                   : code_bits == 16 ? rope_kernel<16>
                   : code_bits == 8  ? rope_kernel<8>
                                     : rope_kernel<4>;
-    kernel<<<num_tokens, kThreads, 0, stream>>>(p);
+    kernel<<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
