@@ -847,10 +847,11 @@ struct SelectLayout {
     size_t keys_offset, sums_offset, total;
 };
 
-int64_t select_chunks(int64_t vocab, int values) { return (vocab + values - 1) / values; }
+constexpr int kSelectMinChunk = 2048;  // values of a row that are worth a CTA
+int64_t select_chunks(int64_t vocab) { return (vocab + kSelectMinChunk - 1) / kSelectMinChunk; }
 
 SelectLayout select_layout(int64_t groups, int64_t width, int64_t vocab, int64_t picks) {
-    const int64_t lists = groups * width * select_chunks(vocab, beam_select_chunk_values(false));
+    const int64_t lists = groups * width * select_chunks(vocab);
     SelectLayout w{};
     w.keys_offset = kSelectCounterBytes;
     w.sums_offset = w.keys_offset + align256(static_cast<size_t>(lists * picks * 8));
@@ -864,9 +865,16 @@ int check_select(int32_t groups, int32_t width, int32_t vocab, int32_t picks) {
     if (width > kMaxBeamWidth || picks > kMaxBeamWidth || vocab > (1 << 26)) return SA_ERR_UNSUPPORTED;
     if (groups > kSelectMaxGroups) return SA_ERR_UNSUPPORTED;
     // the finest cut's CTAs fit a grid
-    if (static_cast<int64_t>(groups) * width * select_chunks(vocab, beam_select_chunk_values(false)) > INT32_MAX)
+    if (static_cast<int64_t>(groups) * width * select_chunks(vocab) > INT32_MAX)
         return SA_ERR_UNSUPPORTED;
     return SA_OK;
+}
+
+// Chunks of a row: one to four CTAs on every SM, within the sizes that a CTA takes.
+int32_t select_cut(int64_t rows, int64_t vocab, int max_chunk, int sms) {
+    const int64_t least = (vocab + max_chunk - 1) / max_chunk;
+    const int64_t want = (4 * static_cast<int64_t>(sms) + rows - 1) / rows;
+    return static_cast<int32_t>(std::max(least, std::min(want, select_chunks(vocab))));
 }
 
 }  // namespace
@@ -891,11 +899,7 @@ static int select_impl(const void *logits, bool bf16, int64_t logits_stride, con
     if (workspace == nullptr || workspace_bytes < w.total || !aligned(workspace, 256)) return SA_ERR_WORKSPACE;
     const int sms = device_sm_count();
     if (sms <= 0) return SA_ERR_CUDA;
-    // 32 values a thread where that gives every SM two CTAs, else 8, so that
-    // few rows spread over more SMs
-    const int64_t rows = static_cast<int64_t>(num_groups) * beam_width;
-    const bool large = rows * select_chunks(vocab, beam_select_chunk_values(true)) >= 2 * sms;
-    const int values = beam_select_chunk_values(large);
+    const bool rows_aligned = aligned(logits, 16) && logits_stride * (bf16 ? 2 : 4) % 16 == 0;
     SelectParams p{};
     p.logits = logits;
     p.stride = logits_stride;
@@ -914,12 +918,11 @@ static int select_impl(const void *logits, bool bf16, int64_t logits_stride, con
     p.V = vocab;
     p.K = num_select;
     p.eos = eos_token;
-    // even chunks, in 16-byte groups
-    p.n_chunks = static_cast<int32_t>(select_chunks(vocab, values));
-    p.chunk = ((vocab + p.n_chunks - 1) / p.n_chunks + 7) / 8 * 8;
-    const bool rows_aligned = aligned(logits, 16) && logits_stride * (bf16 ? 2 : 4) % 16 == 0;
+    p.n_chunks = select_cut(static_cast<int64_t>(num_groups) * beam_width, vocab,
+                            beam_select_max_chunk(bf16, rows_aligned), sms);
+    p.chunk = ((vocab + p.n_chunks - 1) / p.n_chunks + 7) / 8 * 8;  // even, in 16-byte pieces
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_beam_select(p, bf16, large, rows_aligned, s) != cudaSuccess) return SA_ERR_CUDA;
+    if (launch_beam_select(p, bf16, rows_aligned, s) != cudaSuccess) return SA_ERR_CUDA;
     return finish(s, nullptr);
 }
 

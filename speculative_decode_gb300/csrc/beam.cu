@@ -8,19 +8,24 @@
 // to the larger logit, then the lower token. A NaN logit counts as -inf, +inf as the
 // largest finite value.
 //
-// One pass over the logits: a CTA keeps a chunk of a row in registers, and takes
-// from it the chunk's maximum, the sum of exp(x - max) and its K largest
-// logits (a row's order is its logits' order, so no sum is needed to choose
-// them). The last CTA of a group to finish (one atomic counter a group, no
-// spinning) merges the sums into each row's lse and the chunks' picks into the
-// group's. lse and the values are formed in 64 bits, so that beams are told
-// apart down to the accuracy of the sums (about 1e-7).
+// One pass over the logits: a CTA streams a chunk of a row in batches of 16
+// bytes x 4 a thread, the next batch's loads in flight while one is summed.
+// Each thread carries its maximum and its sum of exp(x - max), and keeps every
+// batch's maximum in shared memory. The K largest logits are found afterwards (a
+// row's order is its logits' order, so no sum is needed to choose them): each
+// of the eight warps finds its J-th largest lane maximum, J = ceil(K / 8); at
+// least J values of each warp reach the least of those, so the K largest of
+// the chunk do. The batches whose maximum reaches it (about 20 for K = 8) are
+// read again, from the L2, and their values that reach it ranked by counting.
+// When many do (heavy ties) the lowest tokens among the equal ones are taken in
+// order, and otherwise the values one by one as block-wide maxima.
 //
-// Choosing K of a chunk: each of the eight warps finds its J-th largest lane
-// maximum, J = ceil(K / 8). At least J values of each warp reach the least of
-// those, so the K largest of the chunk do; the few values that reach it (about
-// 20 for K = 8) are collected and ranked by counting. When more than 128 do
-// (constant rows, heavy ties), they are taken one by one as block-wide maxima.
+// The last CTA of a group to finish (one atomic counter a group, no spinning)
+// merges the sums into each row's lse and the chunks' picks into the group's.
+// lse and the values are formed in 64 bits, so that beams are told apart down
+// to the accuracy of the sums (about 1e-7). Bound: the logits' bytes for many
+// rows (the exponentials would take a third of that time); for few the chain of a
+// load, a second one, the counter and the merge.
 //
 // Reordering. Child i of a group continues beam p = parents[i]. Pages that are
 // full are shared: the child's table row starts with its parent's. The pages
@@ -30,7 +35,6 @@
 // parent's rows of the unfilled page are copied. Nothing that is read is
 // written, so one kernel does it in any order. Bound: bytes copied.
 #include <cfloat>
-#include <type_traits>
 
 #include "common.cuh"
 
@@ -42,7 +46,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;       // collected candidates of a chunk
 constexpr int kRankMost = 128;   // ranked by counting up to this many
-constexpr int kMergeCap = 2048;  // candidates of one merge step
+constexpr int kMergeCap = 1024;  // candidates of one merge step
+constexpr int kMaxBatches = 16;  // batches of a chunk
 constexpr int kMaxBeams = kMaxBeamWidth;
 constexpr int kIndexBits = 27;   // tokens in a merge key
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
@@ -82,33 +87,86 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     return static_cast<uint64_t>(top) << 32 | lo;
 }
 
+// NaN -> -inf, +inf -> largest finite
+__device__ __forceinline__ float tamed(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 struct Logits32 {
     using type = float;
-    static constexpr int kVec = 4;
+    static constexpr int kVec = 4;  // values of 16 bytes
+    static constexpr uint32_t kNone = 0xff800000u;
     static __device__ __forceinline__ float one(const float *p) { return *p; }
-    static __device__ __forceinline__ void vec(const float *p, float *x) {
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-        x[0] = v.x;
-        x[1] = v.y;
-        x[2] = v.z;
-        x[3] = v.w;
+    template <int E>
+    static __device__ __forceinline__ float value(const uint4 &v) {
+        return __uint_as_float(E == 0 ? v.x : E == 1 ? v.y : E == 2 ? v.z : v.w);
     }
 };
 
 struct Logits16 {
     using type = uint16_t;
     static constexpr int kVec = 8;
+    static constexpr uint32_t kNone = 0xff80ff80u;
     static __device__ __forceinline__ float one(const uint16_t *p) {
         return __uint_as_float(static_cast<uint32_t>(*p) << 16);
     }
-    static __device__ __forceinline__ void vec(const uint16_t *p, float *x) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    template <int E>
+    static __device__ __forceinline__ float value(const uint4 &v) {
+        const uint32_t w = E < 2 ? v.x : E < 4 ? v.y : E < 6 ? v.z : v.w;
+        return E & 1 ? bf16_hi(w) : bf16_lo(w);
+    }
+};
+
+// The values of 16 loaded bytes, tamed.
+template <typename L>
+__device__ __forceinline__ void values(const uint4 &v, float (&x)[L::kVec]) {
+    x[0] = tamed(L::template value<0>(v));
+    x[1] = tamed(L::template value<1>(v));
+    x[2] = tamed(L::template value<2>(v));
+    x[3] = tamed(L::template value<3>(v));
+    if constexpr (L::kVec == 8) {
+        x[4] = tamed(L::template value<4>(v));
+        x[5] = tamed(L::template value<5>(v));
+        x[6] = tamed(L::template value<6>(v));
+        x[7] = tamed(L::template value<7>(v));
+    }
+}
+
+// A chunk of a row as the CTA reads it: batches of kLoads pieces of kVec values
+// a thread. kAligned: the row starts on a 16-byte boundary and a piece is 16
+// bytes of consecutive values; otherwise a piece's values are kThreads apart.
+// All rows of a launch are cut alike, whatever their address, so that equal
+// rows have equal sums and equal values.
+template <typename L, bool kAligned>
+struct Chunk {
+    using T = typename L::type;
+    static constexpr int kVec = L::kVec, kLoads = kAligned ? 4 : 16 / L::kVec;
+    static constexpr int kBatch = kThreads * kLoads * kVec;
+    const T *row;
+    int begin, end;
+
+    __device__ __forceinline__ int first(int batch, int i) const {  // of thread t's piece i
+        const int at = begin + batch * kBatch + i * kThreads * kVec;
+        return kAligned ? at + static_cast<int>(threadIdx.x) * kVec : at + static_cast<int>(threadIdx.x);
+    }
+    static __device__ __forceinline__ int step(int e) { return kAligned ? e : e * kThreads; }
+    __device__ __forceinline__ uint4 load(int batch, int i) const {
+        const int at = first(batch, i);
+        if (kAligned && at + kVec <= end) return *reinterpret_cast<const uint4 *>(row + at);
+        uint32_t w[4] = {L::kNone, L::kNone, L::kNone, L::kNone};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16_lo(w[i]);
-            x[2 * i + 1] = bf16_hi(w[i]);
+        for (int e = 0; e < kVec; ++e) {
+            if (at + step(e) >= end) continue;
+            const T *p = row + at + step(e);
+            if constexpr (kVec == 4) w[e] = *reinterpret_cast<const uint32_t *>(p);
+            else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p)) << 16
+                                  : (w[e / 2] & 0xffff0000u) | *reinterpret_cast<const uint16_t *>(p);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -130,8 +188,8 @@ __device__ __forceinline__ Candidate make_candidate(double value, int beam, uint
 
 struct SelectShared {
     float m[kWarps], s[kWarps];
-    uint64_t tau[kWarps];
-    int n, last;
+    uint32_t tau[kWarps];
+    int n, last, scan[kWarps];
     uint64_t red[2][kWarps];
     // merge
     double lse[kMaxBeams];
@@ -141,12 +199,26 @@ struct SelectShared {
     Candidate best[kMaxBeams];
     int32_t out_token[kMaxBeams], out_beam[kMaxBeams];
     float out_score[kMaxBeams];
+    Candidate kept[kRankMost];
     union {
-        uint64_t keys[kCap];
+        struct {
+            float batch_max[kMaxBatches][kThreads];
+            uint64_t keys[kCap];
+        };
         Candidate cand[kMergeCap];
     };
-    Candidate kept[kRankMost];
 };
+
+// The warp's J-th largest of the lanes' keys (0 where fewer lanes have one).
+__device__ __forceinline__ uint32_t jth_largest(uint32_t key, int J) {
+    uint32_t jth = 0;
+    for (int j = 0; j < J; ++j) {
+        jth = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t who = __ballot_sync(0xffffffffu, key == jth);
+        if (static_cast<int>(threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+    }
+    return jth;
+}
 
 // The K largest of the n candidates in S.cand to S.best, sorted (none: value
 // 0); returns how many there are. Called by the whole block.
@@ -156,22 +228,16 @@ __device__ int merge_best(SelectShared &S, int n, int K) {
     // largest lane maxima (as in a chunk)
     uint32_t top = 0;
     for (int e = t; e < n; e += kThreads) top = max(top, static_cast<uint32_t>(S.cand[e].value >> 32));
-    const int J = (K + kWarps - 1) / kWarps;
-    uint32_t jth = 0;
-    for (int j = 0; j < J; ++j) {
-        jth = __reduce_max_sync(0xffffffffu, top);
-        const uint32_t who = __ballot_sync(0xffffffffu, top == jth);
-        if (lane == __ffs(who) - 1) top = 0;
-    }
+    const uint32_t jth = jth_largest(top, (K + kWarps - 1) / kWarps);
     if (lane == 0) S.tau[warp] = jth;
     if (t == 0) S.n = 0;
     __syncthreads();
-    uint64_t tau = S.tau[0];
+    uint32_t tau = S.tau[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
     for (int e = t; e < n; e += kThreads) {
         const Candidate c = S.cand[e];
-        if (c.value != 0 && (c.value >> 32) >= tau) {
+        if (c.value != 0 && static_cast<uint32_t>(c.value >> 32) >= tau) {
             const int at = atomicAdd(&S.n, 1);
             if (at < kRankMost) S.kept[at] = c;
         }
@@ -266,46 +332,62 @@ __device__ void fill_rest(SelectShared &S, const SelectParams &P, int g, int n) 
 template <typename L>
 __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t row0 = static_cast<int64_t>(g) * P.W;
-    for (int w = warp; w < P.W; w += kWarps) {
-        const float2 *part = P.part_sums + (row0 + w) * P.n_chunks;
-        float m = -INFINITY;
-        for (int c = lane; c < P.n_chunks; c += 32) m = fmaxf(m, __ldcg(part + c).x);
+    const int row0 = g * P.W;
+    const unsigned W = P.W, n_chunks = P.n_chunks;
+    // Candidates in steps of kMergeCap, the best of the steps before kept. Entry
+    // e is of row e % W, so that each warp sees all rows, and goes through a rank
+    // of all the row's chunks before the next. The first step's keys are
+    // loaded while the sums are merged.
+    const unsigned total = W * n_chunks * P.K;
+    auto key_of = [&](unsigned e) {
+        const unsigned w = e % W, at = e / W;
+        return P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + at % n_chunks) * P.K + at / n_chunks;
+    };
+    constexpr int kMine = kMergeCap / kThreads;
+    uint64_t mine[kMine];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        double s = 0.0;
+    for (int u = 0; u < kMine; ++u) mine[u] = t + u * kThreads < total ? __ldcg(key_of(t + u * kThreads)) : 0;
+    for (int w = warp; w < P.W; w += kWarps) {
+        const float2 *part = P.part_sums + static_cast<int64_t>(row0 + w) * P.n_chunks;
+        float m = -INFINITY, s = 0.f;
         for (int c = lane; c < P.n_chunks; c += 32) {
             const float2 q = __ldcg(part + c);
-            if (q.x > -INFINITY) s += static_cast<double>(q.y) * static_cast<double>(expf(q.x - m));
+            if (q.x > m) {
+                s = fmaf(s, m > -INFINITY ? expf(m - q.x) : 0.f, q.y);
+                m = q.x;
+            } else if (q.x > -INFINITY) {
+                s = fmaf(q.y, expf(q.x - m), s);
+            }
         }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, order32(m));
+        const float row_m = order32_value(top);
+        double sum = m > -INFINITY ? static_cast<double>(s) * static_cast<double>(expf(m - row_m)) : 0.0;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
-            S.row_m[w] = m;
-            S.row_s[w] = s;
+            S.row_m[w] = row_m;
+            S.row_s[w] = sum;
         }
     }
     __syncthreads();
     if (t < P.W) S.lse[t] = static_cast<double>(S.row_m[t]) + log(S.row_s[t]);
     __syncthreads();
 
-    // candidates in steps of kMergeCap, the best of the steps before kept;
-    // consecutive candidates are of different rows, so that each warp sees all
-    const int64_t total = static_cast<int64_t>(P.n_chunks) * P.K * P.W;
     int n = 0;
-    for (int64_t e0 = 0; e0 < total;) {
-        const int take = static_cast<int>(min(total - e0, static_cast<int64_t>(kMergeCap - n)));
+    for (unsigned e0 = 0; e0 < total;) {
+        const int take = static_cast<int>(min(total - e0, static_cast<unsigned>(kMergeCap - n)));
         if (t < n) S.cand[t] = S.best[t];
-        for (int i = t; i < take; i += kThreads) {
-            const int w = static_cast<int>((e0 + i) % P.W), at = static_cast<int>((e0 + i) / P.W);
-            const int64_t row = row0 + w;
-            const float score = P.scores[row];
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int i = t + u * kThreads;
+            if (i >= take) continue;
+            const unsigned w = (e0 + i) % W;
+            const float score = P.scores[row0 + w];
             Candidate c{0, 0};
-            if (P.finished != nullptr && P.finished[row] != 0) {
-                if (at == 0) c = make_candidate(score, w, ~0u, P.eos);
+            if (P.finished != nullptr && P.finished[row0 + w] != 0) {
+                if (e0 + i < W) c = make_candidate(score, w, ~0u, P.eos);
             } else {
-                // a rank of all the row's chunks, then the next
-                const uint64_t key = __ldcg(P.part_keys + (row * P.n_chunks + at % P.n_chunks) * P.K + at / P.n_chunks);
+                const uint64_t key = e0 == 0 ? mine[u] : __ldcg(key_of(e0 + i));
                 if (key != 0) {
                     const uint32_t order = static_cast<uint32_t>(key >> 32);
                     c = make_candidate(score + (static_cast<double>(order32_value(order)) - S.lse[w]), w, order,
@@ -345,142 +427,207 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     }
 }
 
-// E values of a row per thread. kAligned: every row starts on a 16-byte
-// boundary and is read in 16-byte groups.
-template <typename L, int E, bool kAligned>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const SelectParams P) {
-    using T = typename L::type;
-    constexpr int kVec = L::kVec;
-    __shared__ SelectShared S;
+// The chunk's K largest values as keys, best first, to out (0: none). tau: the
+// threshold that at least K values reach (0: fewer than K lanes have a value,
+// every value is collected).
+template <typename C, typename L>
+__device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, int batches, uint32_t tau, int K,
+                                             uint64_t *out) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t row = blockIdx.x / P.n_chunks;
-    const int chunk = static_cast<int>(blockIdx.x - row * P.n_chunks);
-    const int g = static_cast<int>(row / P.W);
-
-    if (P.finished == nullptr || P.finished[row] == 0) {
-        // All rows of a launch are cut alike, whatever their address, so that
-        // equal rows have equal sums and equal values.
-        const T *x0 = static_cast<const T *>(P.logits) + row * P.stride;
-        const int c0 = chunk * P.chunk, c1 = min(P.V, c0 + P.chunk);
-        auto index = [&](int e) {
-            return c0 + (kAligned ? (t + e / kVec * kThreads) * kVec + e % kVec : t + e * kThreads);
-        };
-        float x[E];
-        if constexpr (kAligned) {
+    const float at_least = tau <= kOrderNegInf ? -INFINITY : order32_value(tau);
+    // f(x, token) of the thread's values in the batches whose maximum reaches x_min
+    auto visit = [&](float x_min, auto &&f) {
+        for (int b = 0; b < batches; ++b) {
+            const float top = S.batch_max[b][t];
+            if (!(top >= x_min && top > -INFINITY)) continue;
+            uint4 v[C::kLoads];
 #pragma unroll
-            for (int i = 0; i < E / kVec; ++i) {
-                const int first = index(i * kVec);
-                if (first + kVec <= c1) {
-                    L::vec(x0 + first, x + i * kVec);
-                } else {
+            for (int i = 0; i < C::kLoads; ++i) v[i] = chunk.load(b, i);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) x[i * kVec + e] = first + e < c1 ? L::one(x0 + first + e) : -INFINITY;
+            for (int i = 0; i < C::kLoads; ++i) {
+                float x[C::kVec];
+                values<L>(v[i], x);
+                const int first = chunk.first(b, i);
+#pragma unroll
+                for (int e = 0; e < C::kVec; ++e)
+                    if (x[e] >= x_min && x[e] > -INFINITY) f(x[e], first + C::step(e));
+            }
+        }
+    };
+    auto collect = [&](float x, int token) {
+        const int to = atomicAdd(&S.n, 1);
+        if (to < kCap) S.keys[to] = pick_key(x, token);
+    };
+    visit(at_least, collect);
+    __syncthreads();
+    int n = S.n;
+    if (n > kCap && at_least > -INFINITY) {
+        // Ties: the values above the threshold, and behind them the K lowest tokens
+        // at it, in the order of the chunk's pieces and threads.
+        __syncthreads();
+        if (t == 0) S.n = 0;
+        __syncthreads();
+        visit(at_least, [&](float x, int token) {
+            if (x > at_least) collect(x, token);
+        });
+        __syncthreads();
+        n = S.n;
+        if (n <= kCap - kMaxBeams) {
+            int got = 0;
+            for (int slot = 0; slot < batches * C::kLoads && got < K; ++slot) {
+                const int b = slot / C::kLoads, i = slot % C::kLoads;
+                // an unaligned piece's values are kThreads apart: one step at a time
+                for (int part = 0; part < (C::step(1) == 1 ? 1 : C::kVec) && got < K; ++part) {
+                    int ties = 0;
+                    float x[C::kVec];
+                    if (S.batch_max[b][t] >= at_least) {
+                        values<L>(chunk.load(b, i), x);
+#pragma unroll
+                        for (int e = 0; e < C::kVec; ++e)
+                            if ((C::step(1) == 1 || e == part) && x[e] == at_least) ++ties;
+                    }
+                    int incl = ties;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += up;
+                    }
+                    if (lane == 31) S.scan[warp] = incl;
+                    __syncthreads();
+                    int rank = got + incl - ties, all = 0;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        if (w < warp) rank += S.scan[w];
+                        all += S.scan[w];
+                    }
+                    if (ties > 0) {
+                        const int first = chunk.first(b, i);
+#pragma unroll
+                        for (int e = 0; e < C::kVec; ++e)
+                            if ((C::step(1) == 1 || e == part) && x[e] == at_least) {
+                                if (rank < K) S.keys[n + rank] = pick_key(x[e], first + C::step(e));
+                                ++rank;
+                            }
+                    }
+                    got += all;
+                    __syncthreads();
                 }
             }
+            n += min(got, K);
         } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = index(e) < c1 ? L::one(x0 + index(e)) : -INFINITY;
+            n = kCap + 1;
         }
-        // NaN -> -inf, +inf -> largest finite
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            x[e] = fminf(fmaxf(x[e], -INFINITY), FLT_MAX);
-            mx = fmaxf(mx, x[e]);
+    }
+    if (n <= kRankMost) {
+        for (int k = n + t; k < K; k += kThreads) out[k] = 0;
+        if (t < n) {
+            const uint64_t key = S.keys[t];
+            int rank = 0;
+            for (int o = 0; o < n; ++o) rank += S.keys[o] > key;
+            if (rank < K) out[rank] = key;
         }
-        int at = INT32_MAX;  // the lane maximum's lowest token
+        return;
+    }
+    uint64_t last = ~0ull;
+    for (int k = 0; k < K; ++k) {
+        uint64_t best = 0;
+        if (n <= kCap) {
+            for (int o = t; o < n; o += kThreads)
+                if (S.keys[o] < last) best = max(best, S.keys[o]);
+        } else {
+            visit(at_least, [&](float x, int token) {
+                const uint64_t key = pick_key(x, token);
+                if (key < last) best = max(best, key);
+            });
+        }
+        best = warp_max(best);
+        if (lane == 0) S.red[k & 1][warp] = best;
+        __syncthreads();
+        last = S.red[k & 1][0];
 #pragma unroll
-        for (int e = E - 1; e >= 0; --e) at = x[e] == mx ? index(e) : at;
+        for (int w = 1; w < kWarps; ++w) last = max(last, S.red[k & 1][w]);
+        if (t == 0) out[k] = last;
+    }
+}
 
-        uint32_t key = order32(mx);
-        const uint32_t wtop = __reduce_max_sync(0xffffffffu, key);
-        const float wmax = order32_value(wtop);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-        if (wtop != kOrderNegInf) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) part[e & 3] += exp2f((x[e] - wmax) * kLog2e);
-        }
-        float sum = (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+template <typename L, bool kAligned>
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectParams P) {
+    using C = Chunk<L, kAligned>;
+    __shared__ SelectShared S;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const unsigned row = blockIdx.x / static_cast<unsigned>(P.n_chunks);
+    const int chunk_at = static_cast<int>(blockIdx.x - row * P.n_chunks);
+    const int g = static_cast<int>(row / static_cast<unsigned>(P.W));
 
-        // the warp's J-th largest lane maximum (lower token first among equals)
-        const int J = (P.K + kWarps - 1) / kWarps;
-        uint64_t jth = 0;
-        for (int j = 0; j < J; ++j) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-            if (top <= kOrderNegInf) {
-                jth = 0;
-                break;
+    if (P.finished == nullptr || P.finished[row] == 0) {
+        C chunk;
+        chunk.row = static_cast<const typename L::type *>(P.logits) + static_cast<int64_t>(row) * P.stride;
+        chunk.begin = chunk_at * P.chunk;
+        chunk.end = min(P.V, chunk.begin + P.chunk);
+        const int batches = (chunk.end - chunk.begin + C::kBatch - 1) / C::kBatch;  // 0 behind the row
+        uint4 next[C::kLoads];
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) next[i] = chunk.load(0, i);
+        float m = -INFINITY, sum = 0.f;
+        for (int b = 0; b < batches; ++b) {
+            uint4 now[C::kLoads];
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) now[i] = next[i];
+            if (b + 1 < batches) {
+#pragma unroll
+                for (int i = 0; i < C::kLoads; ++i) next[i] = chunk.load(b + 1, i);
             }
-            const uint32_t who = __reduce_min_sync(0xffffffffu, key == top ? static_cast<uint32_t>(at) : ~0u);
-            jth = static_cast<uint64_t>(top) << 32 | static_cast<uint32_t>(~who);
-            if (key == top && static_cast<uint32_t>(at) == who) key = 0;
+            float top = -INFINITY;
+            constexpr int kPart = 16 / C::kVec;  // pieces of 16 values
+#pragma unroll
+            for (int i0 = 0; i0 < C::kLoads; i0 += kPart) {
+                float x[kPart][C::kVec];
+                float part_top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) {
+                    values<L>(now[i0 + i], x[i]);
+#pragma unroll
+                    for (int e = 0; e < C::kVec; ++e) part_top = fmaxf(part_top, x[i][e]);
+                }
+                top = fmaxf(top, part_top);
+                const float m_new = fmaxf(m, part_top);
+                const float base = m_new > -INFINITY ? m_new : 0.f;
+                float part[4] = {sum * ex2((m - base) * kLog2e), 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < kPart; ++i)
+#pragma unroll
+                    for (int e = 0; e < C::kVec; ++e) part[e & 3] += ex2((x[i][e] - base) * kLog2e);
+                sum = (part[0] + part[1]) + (part[2] + part[3]);
+                m = m_new;
+            }
+            S.batch_max[b][t] = top;
         }
+        const uint32_t key = order32(m);
+        const float warp_m = order32_value(__reduce_max_sync(0xffffffffu, key));
+        float warp_sum = m > -INFINITY ? sum * ex2((m - warp_m) * kLog2e) : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) warp_sum += __shfl_xor_sync(0xffffffffu, warp_sum, o);
+        const uint32_t jth = jth_largest(key, (P.K + kWarps - 1) / kWarps);
         if (lane == 0) {
-            S.m[warp] = wmax;
-            S.s[warp] = sum;
+            S.m[warp] = warp_m;
+            S.s[warp] = warp_sum;
             S.tau[warp] = jth;
         }
         if (t == 0) S.n = 0;
         __syncthreads();
-        uint64_t tau = S.tau[0];
+        uint32_t tau = S.tau[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
-        // tau 0: some warp has too few; every value above -inf is collected
-        const float tau_x = tau == 0 ? -INFINITY : order32_value(static_cast<uint32_t>(tau >> 32));
-        const int tau_at = tau == 0 ? -1 : static_cast<int>(~static_cast<uint32_t>(tau));
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (x[e] >= tau_x) {
-                if (x[e] > tau_x || index(e) <= tau_at) {
-                    const int to = atomicAdd(&S.n, 1);
-                    if (to < kCap) S.keys[to] = pick_key(x[e], index(e));
-                }
-            }
-        }
-        __syncthreads();
-        const int n = S.n;
-        uint64_t *out = P.part_keys + (row * P.n_chunks + chunk) * P.K;
-        if (n <= kRankMost) {
-            for (int k = n + t; k < P.K; k += kThreads) out[k] = 0;
-            if (t < n) {
-                const uint64_t mine = S.keys[t];
-                int rank = 0;
-                for (int o = 0; o < n; ++o) rank += S.keys[o] > mine;
-                if (rank < P.K) out[rank] = mine;
-            }
-        } else {
-            uint64_t last = ~0ull;
-            for (int k = 0; k < P.K; ++k) {
-                uint64_t best = 0;
-                if (n <= kCap) {
-                    for (int o = t; o < n; o += kThreads)
-                        if (S.keys[o] < last) best = max(best, S.keys[o]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint64_t mine = x[e] > -INFINITY ? pick_key(x[e], index(e)) : 0;
-                        if (mine < last) best = max(best, mine);
-                    }
-                }
-                best = warp_max(best);
-                if (lane == 0) S.red[k & 1][warp] = best;
-                __syncthreads();
-                last = S.red[k & 1][0];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) last = max(last, S.red[k & 1][w]);
-                if (t == 0) out[k] = last;
-            }
-        }
+        const int64_t list = static_cast<int64_t>(row) * P.n_chunks + chunk_at;
         if (t == 0) {
-            float m = S.m[0];
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, S.m[w]);
+            float top = S.m[0];
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, S.m[w]);
             float s = 0.f;
-            if (m > -INFINITY)
-                for (int w = 0; w < kWarps; ++w) s += S.s[w] * exp2f((S.m[w] - m) * kLog2e);
-            P.part_sums[row * P.n_chunks + chunk] = make_float2(m, s);
+            if (top > -INFINITY)
+                for (int w = 0; w < kWarps; ++w) s += S.s[w] * ex2((S.m[w] - top) * kLog2e);
+            P.part_sums[list] = make_float2(top, s);
         }
+        pick_largest<C, L>(S, chunk, batches, tau, P.K, P.part_keys + list * P.K);
     }
 
     // ---- count this CTA; the last one of a group merges
@@ -562,19 +709,14 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const ReorderPar
 
 }  // namespace
 
-int beam_select_chunk_values(bool large) { return kThreads * (large ? 32 : 8); }
+int beam_select_max_chunk(bool bf16, bool aligned) {
+    return kMaxBatches * (bf16 && aligned ? Chunk<Logits16, true>::kBatch : Chunk<Logits32, true>::kBatch);
+}
 
-cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool large, bool aligned, cudaStream_t stream) {
+cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool aligned, cudaStream_t stream) {
     const int64_t ctas = static_cast<int64_t>(p.B) * p.W * p.n_chunks;
-    auto pick = [&](auto logits, auto aligned_rows) {
-        using L = decltype(logits);
-        constexpr bool kAligned = decltype(aligned_rows)::value;
-        return large ? beam_select_kernel<L, 32, kAligned> : beam_select_kernel<L, 8, kAligned>;
-    };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    auto kernel = bf16 ? (aligned ? pick(Logits16{}, Yes{}) : pick(Logits16{}, No{}))
-                       : (aligned ? pick(Logits32{}, Yes{}) : pick(Logits32{}, No{}));
+    auto kernel = bf16 ? (aligned ? beam_select_kernel<Logits16, true> : beam_select_kernel<Logits16, false>)
+                       : (aligned ? beam_select_kernel<Logits32, true> : beam_select_kernel<Logits32, false>);
     kernel<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

@@ -202,8 +202,8 @@ struct SelectParams {
     int32_t B, W, V, K, eos, n_chunks, chunk;
 };
 // aligned: every row starts on a 16-byte boundary
-cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool large, bool aligned, cudaStream_t stream);
-int beam_select_chunk_values(bool large);  // values of a row that one CTA holds
+cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool aligned, cudaStream_t stream);
+int beam_select_max_chunk(bool bf16, bool aligned);  // most values of a row for one CTA
 
 struct ReorderParams {
     const int32_t *parents, *table, *seq_lens;
