@@ -192,6 +192,8 @@ struct SelectShared {
     int n, last, scan[kWarps];
     uint64_t red[2][kWarps];
     // merge
+    float score[kMaxBeams];
+    bool done[kMaxBeams];
     double lse[kMaxBeams];
     float row_m[kMaxBeams];
     double row_s[kMaxBeams];
@@ -208,6 +210,33 @@ struct SelectShared {
         Candidate cand[kMergeCap];
     };
 };
+
+// log(s) of a sum s >= 1 to about 1e-9, with no 64-bit polynomial (64-bit
+// arithmetic is slow here, and every group's merge waits for this). s = 2^k (f +
+// rest), f in [sqrt(1/2), sqrt(2)) a float; log f = 2 atanh(z), z = (f - 1) /
+// (f + 1) in two floats, by its series: z <= 0.172, so z^13 / 13 is below 1e-11.
+__device__ __forceinline__ double log_of_sum(double s) {
+    const float hi = static_cast<float>(s), lo = static_cast<float>(s - static_cast<double>(hi));
+    const uint32_t bits = __float_as_uint(hi);
+    int k = static_cast<int>(bits >> 23) - 127;
+    float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    if (f > 1.41421356f) {
+        f *= 0.5f;
+        ++k;
+    }
+    const float num = f - 1.f;  // exact
+    const float den = f + 1.f, den_lo = f - (den - 1.f);
+    const float z = __fdividef(num, den);
+    const float z_lo = __fdividef(fmaf(-z, den, num) - z * den_lo, den);
+    const float q = z * z;
+    float p = 1.f / 11;
+    p = fmaf(p, q, 1.f / 9);
+    p = fmaf(p, q, 1.f / 7);
+    p = fmaf(p, q, 1.f / 5);
+    p = fmaf(p, q, 1.f / 3);
+    const float small = 2.f * fmaf(p * q, z, z_lo) + __fdividef(lo, hi);
+    return static_cast<double>(k) * 0.69314718055994530942 + (static_cast<double>(2.f * z) + static_cast<double>(small));
+}
 
 // The warp's J-th largest of the lanes' keys (0 where fewer lanes have one).
 __device__ __forceinline__ uint32_t jth_largest(uint32_t key, int J) {
@@ -287,8 +316,7 @@ __device__ void fill_rest(SelectShared &S, const SelectParams &P, int g, int n) 
     const int lane = threadIdx.x & 31;
     for (int w = 0; w < P.W && n < P.K; ++w) {
         const int64_t row = static_cast<int64_t>(g) * P.W + w;
-        const bool live = P.scores[row] > -INFINITY;
-        const bool done = P.finished != nullptr && P.finished[row] != 0;
+        const bool live = S.score[w] > -INFINITY, done = S.done[w];
         auto put = [&](int token) {
             if (lane == 0) {
                 S.out_token[n] = token;
@@ -334,19 +362,30 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int row0 = g * P.W;
     const unsigned W = P.W, n_chunks = P.n_chunks;
-    // Candidates in steps of kMergeCap, the best of the steps before kept. Entry
-    // e is of row e % W, so that each warp sees all rows, and goes through a rank
-    // of all the row's chunks before the next. The first step's keys are
-    // loaded while the sums are merged.
+    // Candidates in steps of kMergeCap, the best of the steps before kept. The
+    // entries are the lists' in turn; consecutive lists are of different rows, shifted
+    // from chunk to chunk, so that every warp sees the best of all rows. The
+    // first step's keys are loaded while the sums are merged.
     const unsigned total = W * n_chunks * P.K;
-    auto key_of = [&](unsigned e) {
-        const unsigned w = e % W, at = e / W;
-        return P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + at % n_chunks) * P.K + at / n_chunks;
+    auto place = [&](unsigned e, unsigned &w, unsigned &chunk, unsigned &rank) {
+        const unsigned list = e / P.K;
+        rank = e - list * P.K;
+        chunk = list / W;
+        w = (list - chunk * W + chunk) % W;
     };
+    auto key_of = [&](unsigned e) {
+        unsigned w, chunk, rank;
+        place(e, w, chunk, rank);
+        return __ldcg(P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + chunk) * P.K + rank);
+    };
+    if (t < P.W) {
+        S.score[t] = P.scores[row0 + t];
+        S.done[t] = P.finished != nullptr && P.finished[row0 + t] != 0;
+    }
     constexpr int kMine = kMergeCap / kThreads;
     uint64_t mine[kMine];
 #pragma unroll
-    for (int u = 0; u < kMine; ++u) mine[u] = t + u * kThreads < total ? __ldcg(key_of(t + u * kThreads)) : 0;
+    for (int u = 0; u < kMine; ++u) mine[u] = t + u * kThreads < total ? key_of(t + u * kThreads) : 0;
     for (int w = warp; w < P.W; w += kWarps) {
         const float2 *part = P.part_sums + static_cast<int64_t>(row0 + w) * P.n_chunks;
         float m = -INFINITY, s = 0.f;
@@ -370,7 +409,7 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
         }
     }
     __syncthreads();
-    if (t < P.W) S.lse[t] = static_cast<double>(S.row_m[t]) + log(S.row_s[t]);
+    if (t < P.W) S.lse[t] = static_cast<double>(S.row_m[t]) + log_of_sum(S.row_s[t]);
     __syncthreads();
 
     int n = 0;
@@ -381,16 +420,16 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
         for (int u = 0; u < kMine; ++u) {
             const int i = t + u * kThreads;
             if (i >= take) continue;
-            const unsigned w = (e0 + i) % W;
-            const float score = P.scores[row0 + w];
+            unsigned w, chunk, rank;
+            place(e0 + i, w, chunk, rank);
             Candidate c{0, 0};
-            if (P.finished != nullptr && P.finished[row0 + w] != 0) {
-                if (e0 + i < W) c = make_candidate(score, w, ~0u, P.eos);
+            if (S.done[w]) {
+                if (chunk == 0 && rank == 0) c = make_candidate(S.score[w], w, ~0u, P.eos);
             } else {
-                const uint64_t key = e0 == 0 ? mine[u] : __ldcg(key_of(e0 + i));
+                const uint64_t key = e0 == 0 ? mine[u] : key_of(e0 + i);
                 if (key != 0) {
                     const uint32_t order = static_cast<uint32_t>(key >> 32);
-                    c = make_candidate(score + (static_cast<double>(order32_value(order)) - S.lse[w]), w, order,
+                    c = make_candidate(S.score[w] + (static_cast<double>(order32_value(order)) - S.lse[w]), w, order,
                                        ~static_cast<uint32_t>(key));
                 }
             }
@@ -411,19 +450,13 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
         fill_rest<L>(S, P, g, n);
     }
     __syncthreads();
-    int ended = 0;
-    if (t < P.K) {
+    if (t < P.K) {  // the scores may be the inputs' buffers: they have been read
         const int64_t at = static_cast<int64_t>(g) * P.K + t;
         const int token = S.out_token[t], beam = S.out_beam[t];
-        ended = token == P.eos || (P.finished != nullptr && P.finished[row0 + beam] != 0);
         P.tokens[at] = token;
         P.parents[at] = beam;
-    }
-    __syncthreads();  // the outputs may be the inputs' buffers
-    if (t < P.K) {
-        const int64_t at = static_cast<int64_t>(g) * P.K + t;
         P.scores_out[at] = S.out_score[t];
-        if (P.finished_out != nullptr) P.finished_out[at] = ended;
+        if (P.finished_out != nullptr) P.finished_out[at] = token == P.eos || S.done[beam];
     }
 }
 
@@ -435,11 +468,18 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
                                              uint64_t *out) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float at_least = tau <= kOrderNegInf ? -INFINITY : order32_value(tau);
-    // f(x, token) of the thread's values in the batches whose maximum reaches x_min
+    // f(x, token) of the thread's values in the batches whose maximum reaches
+    // x_min. The lanes of a warp read their batches, one each, together.
     auto visit = [&](float x_min, auto &&f) {
+        uint32_t left = 0;
         for (int b = 0; b < batches; ++b) {
             const float top = S.batch_max[b][t];
-            if (!(top >= x_min && top > -INFINITY)) continue;
+            left |= static_cast<uint32_t>(top >= x_min && top > -INFINITY) << b;
+        }
+        while (__any_sync(0xffffffffu, left != 0)) {
+            if (left == 0) continue;
+            const int b = __ffs(left) - 1;
+            left &= left - 1;
             uint4 v[C::kLoads];
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) v[i] = chunk.load(b, i);
@@ -633,13 +673,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
     // ---- count this CTA; the last one of a group merges
     __syncthreads();
     if (t == 0) {
-        __threadfence();
-        const int prev = atomicAdd(&P.counters[g], 1);
-        S.last = prev == P.W * P.n_chunks - 1;
+        S.last = atomic_add_acq_rel(&P.counters[g], 1) == P.W * P.n_chunks - 1;
     }
     __syncthreads();
     if (!S.last) return;
-    __threadfence();
     merge_group<L>(S, P, g);
     if (t == 0) P.counters[g] = 0;
 }

@@ -124,6 +124,14 @@ __device__ __forceinline__ int atomic_add_release(int32_t *p, int v) {
     return old;
 }
 
+// atomicAdd that also acquires: with a block barrier before and after it, the
+// block sees what the blocks that added before have written.
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t *p, int v) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
