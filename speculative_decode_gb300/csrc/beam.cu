@@ -46,7 +46,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;       // collected candidates of a chunk
 constexpr int kRankMost = 128;   // ranked by counting up to this many
-constexpr int kMergeCap = 1024;  // candidates of one merge step
+constexpr int kMergeCap = 1024;  // entries of one merge step
 constexpr int kMaxBatches = 16;  // batches of a chunk
 constexpr int kMaxBeams = kMaxBeamWidth;
 constexpr int kIndexBits = 27;   // tokens in a merge key
@@ -191,32 +191,34 @@ struct SelectShared {
     uint32_t tau[kWarps];
     int n, last, scan[kWarps];
     uint64_t red[2][kWarps];
+    int rank[kRankMost];
+    float batch_max[kMaxBatches][kThreads];
+    uint64_t keys[kCap];
     // merge
     float score[kMaxBeams];
     bool done[kMaxBeams];
     double lse[kMaxBeams];
-    float row_m[kMaxBeams];
-    double row_s[kMaxBeams];
+    float row_m[kMaxBeams], row_s[kMaxBeams], row_lo[kMaxBeams];
+    uint8_t beam_of[kRankMost];
+    Candidate kept[kRankMost];
     Candidate cred[2][kWarps];
     Candidate best[kMaxBeams];
     int32_t out_token[kMaxBeams], out_beam[kMaxBeams];
     float out_score[kMaxBeams];
-    Candidate kept[kRankMost];
-    union {
-        struct {
-            float batch_max[kMaxBatches][kThreads];
-            uint64_t keys[kCap];
-        };
-        Candidate cand[kMergeCap];
-    };
 };
 
-// log(s) of a sum s >= 1 to about 1e-9, with no 64-bit polynomial (64-bit
-// arithmetic is slow here, and every group's merge waits for this). s = 2^k (f +
-// rest), f in [sqrt(1/2), sqrt(2)) a float; log f = 2 atanh(z), z = (f - 1) /
-// (f + 1) in two floats, by its series: z <= 0.172, so z^13 / 13 is below 1e-11.
-__device__ __forceinline__ double log_of_sum(double s) {
-    const float hi = static_cast<float>(s), lo = static_cast<float>(s - static_cast<double>(hi));
+// The sum of two floats as a float and the rest.
+__device__ __forceinline__ void add_exactly(float &hi, float &lo, float other_hi, float other_lo) {
+    const float sum = hi + other_hi, part = sum - hi;
+    lo += other_lo + ((hi - (sum - part)) + (other_hi - part));
+    hi = sum;
+}
+
+// log(hi + lo) of a sum of at least 1 to a few 1e-9, with no 64-bit polynomial
+// (64-bit arithmetic is slow here, and every group's merge waits for this). hi =
+// 2^k f, f in [sqrt(1/2), sqrt(2)); log f = 2 atanh(z), z = (f - 1) / (f + 1) in two
+// floats, by its series: z <= 0.172, so the terms left out are below 1e-10.
+__device__ __forceinline__ double log_of_sum(float hi, float lo) {
     const uint32_t bits = __float_as_uint(hi);
     int k = static_cast<int>(bits >> 23) - 127;
     float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
@@ -247,64 +249,6 @@ __device__ __forceinline__ uint32_t jth_largest(uint32_t key, int J) {
         if (static_cast<int>(threadIdx.x & 31) == __ffs(who) - 1) key = 0;
     }
     return jth;
-}
-
-// The K largest of the n candidates in S.cand to S.best, sorted (none: value
-// 0); returns how many there are. Called by the whole block.
-__device__ int merge_best(SelectShared &S, int n, int K) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    // threshold on the values' upper halves: the least of the warps' J-th
-    // largest lane maxima (as in a chunk)
-    uint32_t top = 0;
-    for (int e = t; e < n; e += kThreads) top = max(top, static_cast<uint32_t>(S.cand[e].value >> 32));
-    const uint32_t jth = jth_largest(top, (K + kWarps - 1) / kWarps);
-    if (lane == 0) S.tau[warp] = jth;
-    if (t == 0) S.n = 0;
-    __syncthreads();
-    uint32_t tau = S.tau[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
-    for (int e = t; e < n; e += kThreads) {
-        const Candidate c = S.cand[e];
-        if (c.value != 0 && static_cast<uint32_t>(c.value >> 32) >= tau) {
-            const int at = atomicAdd(&S.n, 1);
-            if (at < kRankMost) S.kept[at] = c;
-        }
-    }
-    __syncthreads();
-    const int got = S.n;
-    if (got <= kRankMost) {
-        if (t < got) {
-            const Candidate c = S.kept[t];
-            int rank = 0;
-            for (int o = 0; o < got; ++o) rank += before(S.kept[o], c);
-            if (rank < K) S.best[rank] = c;
-        }
-        __syncthreads();
-        return min(got, K);
-    }
-    Candidate last{~0ull, ~0ull};
-    for (int k = 0; k < K; ++k) {
-        Candidate c{0, 0};
-        for (int e = t; e < n; e += kThreads) {
-            const Candidate x = S.cand[e];
-            if (before(last, x) && before(x, c)) c = x;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const Candidate x{__shfl_xor_sync(0xffffffffu, c.value, o), __shfl_xor_sync(0xffffffffu, c.rest, o)};
-            if (before(x, c)) c = x;
-        }
-        if (lane == 0) S.cred[k & 1][warp] = c;
-        __syncthreads();
-        last = S.cred[k & 1][0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w)
-            if (before(S.cred[k & 1][w], last)) last = S.cred[k & 1][w];
-        if (t == 0) S.best[k] = last;
-    }
-    __syncthreads();
-    return K;  // more than K candidates have a value
 }
 
 // The slots behind the `n` continuations of a value above -inf: continuations
@@ -361,83 +305,167 @@ template <typename L>
 __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int row0 = g * P.W;
-    const unsigned W = P.W, n_chunks = P.n_chunks;
-    // Candidates in steps of kMergeCap, the best of the steps before kept. The
-    // entries are the lists' in turn; consecutive lists are of different rows, shifted
-    // from chunk to chunk, so that every warp sees the best of all rows. The
-    // first step's keys are loaded while the sums are merged.
-    const unsigned total = W * n_chunks * P.K;
-    auto place = [&](unsigned e, unsigned &w, unsigned &chunk, unsigned &rank) {
-        const unsigned list = e / P.K;
-        rank = e - list * P.K;
-        chunk = list / W;
+    const unsigned W = P.W, n_chunks = P.n_chunks, K = P.K;
+    // Entries in steps of kMergeCap, the best of the steps before kept. They are
+    // the lists' in turn, consecutive lists of different rows, shifted from chunk
+    // to chunk; entry 8 q + r of a step goes to lane q of warp (q + r) % 8. So every
+    // warp sees the best of all rows, however many there are. The first step's
+    // keys are loaded while the sums are merged.
+    const unsigned total = W * n_chunks * K;
+    auto place = [&](unsigned e, unsigned &w, unsigned &list_at) {
+        const unsigned list = e / K, chunk = list / W;
         w = (list - chunk * W + chunk) % W;
+        list_at = chunk * K + (e - list * K);
+    };
+    auto entry_of = [&](int u) {
+        const unsigned q = u * 32 + lane;
+        return 8 * q + ((warp - q) & 7);
     };
     auto key_of = [&](unsigned e) {
-        unsigned w, chunk, rank;
-        place(e, w, chunk, rank);
-        return __ldcg(P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + chunk) * P.K + rank);
+        unsigned w, list_at;
+        place(e, w, list_at);
+        return __ldcg(P.part_keys + static_cast<int64_t>(row0 + w) * n_chunks * K + list_at);
     };
+    constexpr int kMine = kMergeCap / kThreads;
+    uint64_t mine[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) mine[u] = entry_of(u) < total ? key_of(entry_of(u)) : 0;
     if (t < P.W) {
         S.score[t] = P.scores[row0 + t];
         S.done[t] = P.finished != nullptr && P.finished[row0 + t] != 0;
     }
-    constexpr int kMine = kMergeCap / kThreads;
-    uint64_t mine[kMine];
-#pragma unroll
-    for (int u = 0; u < kMine; ++u) mine[u] = t + u * kThreads < total ? key_of(t + u * kThreads) : 0;
     for (int w = warp; w < P.W; w += kWarps) {
         const float2 *part = P.part_sums + static_cast<int64_t>(row0 + w) * P.n_chunks;
-        float m = -INFINITY, s = 0.f;
+        float m = -INFINITY, s = 0.f, s_lo = 0.f;
         for (int c = lane; c < P.n_chunks; c += 32) {
             const float2 q = __ldcg(part + c);
             if (q.x > m) {
-                s = fmaf(s, m > -INFINITY ? expf(m - q.x) : 0.f, q.y);
+                const float f = m > -INFINITY ? expf(m - q.x) : 0.f;
+                s *= f;
+                s_lo *= f;
+                add_exactly(s, s_lo, q.y, 0.f);
                 m = q.x;
             } else if (q.x > -INFINITY) {
-                s = fmaf(q.y, expf(q.x - m), s);
+                add_exactly(s, s_lo, q.y * expf(q.x - m), 0.f);
             }
         }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, order32(m));
-        const float row_m = order32_value(top);
-        double sum = m > -INFINITY ? static_cast<double>(s) * static_cast<double>(expf(m - row_m)) : 0.0;
+        const float row_m = order32_value(__reduce_max_sync(0xffffffffu, order32(m)));
+        const float f = m > -INFINITY ? expf(m - row_m) : 0.f;
+        s *= f;
+        s_lo *= f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o >= 1; o >>= 1)
+            add_exactly(s, s_lo, __shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, s_lo, o));
         if (lane == 0) {
             S.row_m[w] = row_m;
-            S.row_s[w] = sum;
+            S.row_s[w] = s;
+            S.row_lo[w] = s_lo;
         }
     }
     __syncthreads();
-    if (t < P.W) S.lse[t] = static_cast<double>(S.row_m[t]) + log_of_sum(S.row_s[t]);
+    if (t < P.W) S.lse[t] = static_cast<double>(S.row_m[t]) + log_of_sum(S.row_s[t], S.row_lo[t]);
     __syncthreads();
 
+    // an entry's candidate, in 64 bits
+    auto candidate = [&](uint64_t key, unsigned w) {
+        if (S.done[w]) return make_candidate(S.score[w], w, ~0u, P.eos);
+        const uint32_t order = static_cast<uint32_t>(key >> 32);
+        return make_candidate(S.score[w] + (static_cast<double>(order32_value(order)) - S.lse[w]), w, order,
+                              ~static_cast<uint32_t>(key));
+    };
     int n = 0;
-    for (unsigned e0 = 0; e0 < total;) {
-        const int take = static_cast<int>(min(total - e0, static_cast<unsigned>(kMergeCap - n)));
-        if (t < n) S.cand[t] = S.best[t];
+    for (unsigned e0 = 0; e0 < total; e0 += kMergeCap) {
+        // The values in 32 bits, with bounds on their errors, leave few to be
+        // computed in 64: those that may reach what K values surely reach.
+        float most[kMine];
+        uint32_t least = 0;
+        unsigned of[kMine];
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
-            const int i = t + u * kThreads;
-            if (i >= take) continue;
-            unsigned w, chunk, rank;
-            place(e0 + i, w, chunk, rank);
-            Candidate c{0, 0};
-            if (S.done[w]) {
-                if (chunk == 0 && rank == 0) c = make_candidate(S.score[w], w, ~0u, P.eos);
-            } else {
-                const uint64_t key = e0 == 0 ? mine[u] : key_of(e0 + i);
-                if (key != 0) {
-                    const uint32_t order = static_cast<uint32_t>(key >> 32);
-                    c = make_candidate(S.score[w] + (static_cast<double>(order32_value(order)) - S.lse[w]), w, order,
-                                       ~static_cast<uint32_t>(key));
+            const unsigned e = e0 + entry_of(u);
+            most[u] = -INFINITY;
+            of[u] = 0;
+            if (e0 > 0) mine[u] = e < total ? key_of(e) : 0;
+            if (e >= total) continue;
+            unsigned w, list_at;
+            place(e, w, list_at);
+            of[u] = w;
+            const float score = S.score[w];
+            if (S.done[w]) mine[u] = list_at == 0 ? 1 : 0;
+            if (mine[u] == 0 || !(score > -INFINITY)) {
+                mine[u] = 0;
+                continue;
+            }
+            float value = score, err = 0.f;
+            if (!S.done[w]) {
+                const float x = order32_value(static_cast<uint32_t>(mine[u] >> 32)), lse = static_cast<float>(S.lse[w]);
+                value = score + (x - lse);
+                err = (fabsf(x) + fabsf(lse) + fabsf(score)) * 0x1p-22f;
+            }
+            most[u] = value + err;
+            const float low = value - err;
+            if (low > -INFINITY) least = max(least, order32(low));
+        }
+        const uint32_t jth = jth_largest(least, (K + kWarps - 1) / kWarps);
+        if (lane == 0) S.tau[warp] = jth;
+        if (t == 0) S.n = n;
+        if (t < kRankMost) S.rank[t] = 0;
+        if (t < n) S.kept[t] = S.best[t];
+        __syncthreads();
+        uint32_t tau = S.tau[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
+        const float floor = tau <= kOrderNegInf ? -INFINITY : order32_value(tau);
+#pragma unroll
+        for (int u = 0; u < kMine; ++u)
+            if (mine[u] != 0 && !(most[u] < floor)) {
+                const int at = atomicAdd(&S.n, 1);
+                if (at < kRankMost) {
+                    S.keys[at] = mine[u];
+                    S.beam_of[at] = static_cast<uint8_t>(of[u]);
                 }
             }
-            S.cand[n + i] = c;
+        __syncthreads();
+        const int got = S.n;
+        if (got <= kRankMost) {
+            if (t >= n && t < got) S.kept[t] = candidate(S.keys[t], S.beam_of[t]);
+            __syncthreads();
+            for (int c = lane; c < got; c += 32) {
+                const Candidate mine_c = S.kept[c];
+                int ahead = 0;
+                for (int o = warp; o < got; o += kWarps) ahead += before(S.kept[o], mine_c);
+                if (ahead != 0) atomicAdd(&S.rank[c], ahead);
+            }
+            __syncthreads();
+            if (t < got && S.rank[t] < static_cast<int>(K)) S.best[S.rank[t]] = S.kept[t];
+            n = min(got, static_cast<int>(K));
+        } else {  // one by one
+            Candidate all[kMine + 1];
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) all[u] = mine[u] != 0 ? candidate(mine[u], of[u]) : Candidate{0, 0};
+            all[kMine] = t < n ? S.kept[t] : Candidate{0, 0};
+            Candidate last{~0ull, ~0ull};
+            for (int k = 0; k < static_cast<int>(K); ++k) {
+                Candidate c{0, 0};
+#pragma unroll
+                for (int u = 0; u <= kMine; ++u)
+                    if (before(last, all[u]) && before(all[u], c)) c = all[u];
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) {
+                    const Candidate x{__shfl_xor_sync(0xffffffffu, c.value, o), __shfl_xor_sync(0xffffffffu, c.rest, o)};
+                    if (before(x, c)) c = x;
+                }
+                if (lane == 0) S.cred[k & 1][warp] = c;
+                __syncthreads();
+                last = S.cred[k & 1][0];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w)
+                    if (before(S.cred[k & 1][w], last)) last = S.cred[k & 1][w];
+                if (t == 0) S.best[k] = last;
+            }
+            n = static_cast<int>(K);  // more than K entries have a value
         }
         __syncthreads();
-        n = merge_best(S, n + take, P.K);
-        e0 += take;
     }
     if (t < n) {
         const Candidate c = S.best[t];
@@ -560,12 +588,14 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
     }
     if (n <= kRankMost) {
         for (int k = n + t; k < K; k += kThreads) out[k] = 0;
-        if (t < n) {
-            const uint64_t key = S.keys[t];
-            int rank = 0;
-            for (int o = 0; o < n; ++o) rank += S.keys[o] > key;
-            if (rank < K) out[rank] = key;
+        for (int c = lane; c < n; c += 32) {
+            const uint64_t key = S.keys[c];
+            int ahead = 0;
+            for (int o = warp; o < n; o += kWarps) ahead += S.keys[o] > key;
+            if (ahead != 0) atomicAdd(&S.rank[c], ahead);
         }
+        __syncthreads();
+        if (t < n && S.rank[t] < K) out[S.rank[t]] = S.keys[t];
         return;
     }
     uint64_t last = ~0ull;
@@ -600,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
     const int g = static_cast<int>(row / static_cast<unsigned>(P.W));
 
     if (P.finished == nullptr || P.finished[row] == 0) {
+        if (t == 0 && chunk_at == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.scores + row));  // for the merge
         C chunk;
         chunk.row = static_cast<const typename L::type *>(P.logits) + static_cast<int64_t>(row) * P.stride;
         chunk.begin = chunk_at * P.chunk;
@@ -654,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
             S.tau[warp] = jth;
         }
         if (t == 0) S.n = 0;
+        if (t < kRankMost) S.rank[t] = 0;
         __syncthreads();
         uint32_t tau = S.tau[0];
 #pragma unroll
