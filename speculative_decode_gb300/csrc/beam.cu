@@ -121,52 +121,98 @@ struct Logits16 {
     }
 };
 
-// The values of 16 loaded bytes, tamed.
-template <typename L>
-__device__ __forceinline__ void values(const uint4 &v, float (&x)[L::kVec]) {
-    x[0] = tamed(L::template value<0>(v));
-    x[1] = tamed(L::template value<1>(v));
-    x[2] = tamed(L::template value<2>(v));
-    x[3] = tamed(L::template value<3>(v));
-    if constexpr (L::kVec == 8) {
-        x[4] = tamed(L::template value<4>(v));
-        x[5] = tamed(L::template value<5>(v));
-        x[6] = tamed(L::template value<6>(v));
-        x[7] = tamed(L::template value<7>(v));
-    }
-}
+// 16 bytes of a row from any address: the two aligned 16-byte words that hold
+// them, or (at a row's ends, where those words reach outside) the values
+// themselves in the first.
+template <bool kAligned>
+struct Piece;
+template <>
+struct Piece<true> {
+    uint4 a;
+};
+template <>
+struct Piece<false> {
+    uint4 a, b;
+    bool end;
+};
 
-// A chunk of a row as the CTA reads it: batches of kLoads pieces of kVec values
-// a thread. kAligned: the row starts on a 16-byte boundary and a piece is 16
-// bytes of consecutive values; otherwise a piece's values are kThreads apart.
-// All rows of a launch are cut alike, whatever their address, so that equal
-// rows have equal sums and equal values.
+// A chunk of a row as the CTA reads it: batches of kLoads pieces of kVec
+// consecutive values a thread. kAligned: every row of the launch starts on a
+// 16-byte boundary. All rows of a launch are cut alike, whatever their address,
+// so that equal rows have equal sums and equal values.
 template <typename L, bool kAligned>
 struct Chunk {
     using T = typename L::type;
-    static constexpr int kVec = L::kVec, kLoads = kAligned ? 4 : 16 / L::kVec;
+    static constexpr int kVec = L::kVec, kLoads = kAligned ? 4 : 2;
     static constexpr int kBatch = kThreads * kLoads * kVec;
     const T *row;
-    int begin, end;
+    int begin, end, vocab;
+    int skew;  // bytes of the row's start behind a 16-byte boundary
 
-    __device__ __forceinline__ int first(int batch, int i) const {  // of thread t's piece i
-        const int at = begin + batch * kBatch + i * kThreads * kVec;
-        return kAligned ? at + static_cast<int>(threadIdx.x) * kVec : at + static_cast<int>(threadIdx.x);
+    __device__ __forceinline__ int first(int batch, int i) const {
+        return begin + batch * kBatch + (i * kThreads + static_cast<int>(threadIdx.x)) * kVec;
     }
-    static __device__ __forceinline__ int step(int e) { return kAligned ? e : e * kThreads; }
-    __device__ __forceinline__ uint4 load(int batch, int i) const {
-        const int at = first(batch, i);
-        if (kAligned && at + kVec <= end) return *reinterpret_cast<const uint4 *>(row + at);
+    __device__ __forceinline__ uint4 ends(int at) const {
         uint32_t w[4] = {L::kNone, L::kNone, L::kNone, L::kNone};
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            if (at + step(e) >= end) continue;
-            const T *p = row + at + step(e);
+            if (at + e >= end) continue;
+            const T *p = row + at + e;
             if constexpr (kVec == 4) w[e] = *reinterpret_cast<const uint32_t *>(p);
             else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p)) << 16
                                   : (w[e / 2] & 0xffff0000u) | *reinterpret_cast<const uint16_t *>(p);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ Piece<kAligned> load(int batch, int i) const {
+        const int at = first(batch, i);
+        Piece<kAligned> p;
+        if constexpr (kAligned) {
+            p.a = at + kVec <= end ? *reinterpret_cast<const uint4 *>(row + at) : ends(at);
+        } else {
+            constexpr int kBytes = static_cast<int>(sizeof(T));
+            // the words lie inside the row, and the values inside the chunk
+            p.end = at * kBytes < skew || at + kVec > end || (vocab - at) * static_cast<int64_t>(kBytes) < 32 - skew;
+            if (p.end) {
+                p.a = ends(at);
+            } else {
+                const uint4 *word = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + at) - skew);
+                p.a = word[0];
+                if (skew != 0) p.b = word[1];
+            }
+        }
+        return p;
+    }
+    // The values of a piece, tamed.
+    __device__ __forceinline__ void values(const Piece<kAligned> &p, float (&x)[kVec]) const {
+        uint4 v = p.a;
+        if constexpr (!kAligned) {
+            if (skew != 0 && !p.end) {
+                const uint32_t s = (skew & 3) * 8;
+                const uint32_t w[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
+                switch (skew >> 2) {  // the same for the whole CTA
+                    case 0: v = shifted<0>(w, s); break;
+                    case 1: v = shifted<1>(w, s); break;
+                    case 2: v = shifted<2>(w, s); break;
+                    default: v = shifted<3>(w, s); break;
+                }
+            }
+        }
+        x[0] = tamed(L::template value<0>(v));
+        x[1] = tamed(L::template value<1>(v));
+        x[2] = tamed(L::template value<2>(v));
+        x[3] = tamed(L::template value<3>(v));
+        if constexpr (kVec == 8) {
+            x[4] = tamed(L::template value<4>(v));
+            x[5] = tamed(L::template value<5>(v));
+            x[6] = tamed(L::template value<6>(v));
+            x[7] = tamed(L::template value<7>(v));
+        }
+    }
+    template <int Q>
+    static __device__ __forceinline__ uint4 shifted(const uint32_t (&w)[8], uint32_t s) {
+        return make_uint4(__funnelshift_r(w[Q], w[Q + 1], s), __funnelshift_r(w[Q + 1], w[Q + 2], s),
+                          __funnelshift_r(w[Q + 2], w[Q + 3], s), __funnelshift_r(w[Q + 3], w[Q + 4], s));
     }
 };
 
@@ -313,8 +359,9 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     // keys are loaded while the sums are merged.
     const unsigned total = W * n_chunks * K;
     auto place = [&](unsigned e, unsigned &w, unsigned &list_at) {
-        const unsigned list = e / K, chunk = list / W;
-        w = (list - chunk * W + chunk) % W;
+        const unsigned list = __umulhi(e, P.by_K) + (K == 1 ? e : 0), chunk = __umulhi(list, P.by_W) + (W == 1 ? list : 0);
+        const unsigned turn = list - chunk * W + chunk;
+        w = turn - (__umulhi(turn, P.by_W) + (W == 1 ? turn : 0)) * W;
         list_at = chunk * K + (e - list * K);
     };
     auto entry_of = [&](int u) {
@@ -508,17 +555,17 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
             if (left == 0) continue;
             const int b = __ffs(left) - 1;
             left &= left - 1;
-            uint4 v[C::kLoads];
+            decltype(chunk.load(0, 0)) v[C::kLoads];
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) v[i] = chunk.load(b, i);
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) {
                 float x[C::kVec];
-                values<L>(v[i], x);
+                chunk.values(v[i], x);
                 const int first = chunk.first(b, i);
 #pragma unroll
                 for (int e = 0; e < C::kVec; ++e)
-                    if (x[e] >= x_min && x[e] > -INFINITY) f(x[e], first + C::step(e));
+                    if (x[e] >= x_min && x[e] > -INFINITY) f(x[e], first + e);
             }
         }
     };
@@ -542,44 +589,40 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
         n = S.n;
         if (n <= kCap - kMaxBeams) {
             int got = 0;
-            for (int slot = 0; slot < batches * C::kLoads && got < K; ++slot) {
-                const int b = slot / C::kLoads, i = slot % C::kLoads;
-                // an unaligned piece's values are kThreads apart: one step at a time
-                for (int part = 0; part < (C::step(1) == 1 ? 1 : C::kVec) && got < K; ++part) {
-                    int ties = 0;
-                    float x[C::kVec];
-                    if (S.batch_max[b][t] >= at_least) {
-                        values<L>(chunk.load(b, i), x);
+            for (int piece = 0; piece < batches * C::kLoads && got < K; ++piece) {
+                const int b = piece / C::kLoads, i = piece % C::kLoads;
+                int ties = 0;
+                float x[C::kVec];
+                if (S.batch_max[b][t] >= at_least) {
+                    chunk.values(chunk.load(b, i), x);
 #pragma unroll
-                        for (int e = 0; e < C::kVec; ++e)
-                            if ((C::step(1) == 1 || e == part) && x[e] == at_least) ++ties;
-                    }
-                    int incl = ties;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += up;
-                    }
-                    if (lane == 31) S.scan[warp] = incl;
-                    __syncthreads();
-                    int rank = got + incl - ties, all = 0;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        if (w < warp) rank += S.scan[w];
-                        all += S.scan[w];
-                    }
-                    if (ties > 0) {
-                        const int first = chunk.first(b, i);
-#pragma unroll
-                        for (int e = 0; e < C::kVec; ++e)
-                            if ((C::step(1) == 1 || e == part) && x[e] == at_least) {
-                                if (rank < K) S.keys[n + rank] = pick_key(x[e], first + C::step(e));
-                                ++rank;
-                            }
-                    }
-                    got += all;
-                    __syncthreads();
+                    for (int e = 0; e < C::kVec; ++e) ties += x[e] == at_least;
                 }
+                int incl = ties;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                if (lane == 31) S.scan[warp] = incl;
+                __syncthreads();
+                int rank = got + incl - ties, all = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) rank += S.scan[w];
+                    all += S.scan[w];
+                }
+                if (ties > 0) {
+                    const int first = chunk.first(b, i);
+#pragma unroll
+                    for (int e = 0; e < C::kVec; ++e)
+                        if (x[e] == at_least) {
+                            if (rank < K) S.keys[n + rank] = pick_key(x[e], first + e);
+                            ++rank;
+                        }
+                }
+                got += all;
+                __syncthreads();
             }
             n += min(got, K);
         } else {
@@ -633,15 +676,17 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
         if (t == 0 && chunk_at == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.scores + row));  // for the merge
         C chunk;
         chunk.row = static_cast<const typename L::type *>(P.logits) + static_cast<int64_t>(row) * P.stride;
+        chunk.skew = static_cast<int>(reinterpret_cast<uintptr_t>(chunk.row) & 15);
+        chunk.vocab = P.V;
         chunk.begin = chunk_at * P.chunk;
         chunk.end = min(P.V, chunk.begin + P.chunk);
         const int batches = (chunk.end - chunk.begin + C::kBatch - 1) / C::kBatch;  // 0 behind the row
-        uint4 next[C::kLoads];
+        decltype(chunk.load(0, 0)) next[C::kLoads];
 #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) next[i] = chunk.load(0, i);
         float m = -INFINITY, sum = 0.f;
         for (int b = 0; b < batches; ++b) {
-            uint4 now[C::kLoads];
+            decltype(chunk.load(0, 0)) now[C::kLoads];
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) now[i] = next[i];
             if (b + 1 < batches) {
@@ -649,14 +694,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
                 for (int i = 0; i < C::kLoads; ++i) next[i] = chunk.load(b + 1, i);
             }
             float top = -INFINITY;
-            constexpr int kPart = 16 / C::kVec;  // pieces of 16 values
+            constexpr int kPart = C::kLoads < 16 / C::kVec ? C::kLoads : 16 / C::kVec;  // pieces at once
 #pragma unroll
             for (int i0 = 0; i0 < C::kLoads; i0 += kPart) {
                 float x[kPart][C::kVec];
                 float part_top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < kPart; ++i) {
-                    values<L>(now[i0 + i], x[i]);
+                    chunk.values(now[i0 + i], x[i]);
 #pragma unroll
                     for (int e = 0; e < C::kVec; ++e) part_top = fmaxf(part_top, x[i][e]);
                 }
@@ -779,10 +824,14 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const ReorderPar
 }  // namespace
 
 int beam_select_max_chunk(bool bf16, bool aligned) {
-    return kMaxBatches * (bf16 && aligned ? Chunk<Logits16, true>::kBatch : Chunk<Logits32, true>::kBatch);
+    return kMaxBatches * (bf16 ? (aligned ? Chunk<Logits16, true>::kBatch : Chunk<Logits16, false>::kBatch)
+                               : (aligned ? Chunk<Logits32, true>::kBatch : Chunk<Logits32, false>::kBatch));
 }
 
-cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool aligned, cudaStream_t stream) {
+cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStream_t stream) {
+    // quotients of up to 2^27 as the upper half of a product: exact for divisors up to 32
+    p.by_K = static_cast<uint32_t>(((1ull << 32) + p.K - 1) / p.K);
+    p.by_W = static_cast<uint32_t>(((1ull << 32) + p.W - 1) / p.W);
     const int64_t ctas = static_cast<int64_t>(p.B) * p.W * p.n_chunks;
     auto kernel = bf16 ? (aligned ? beam_select_kernel<Logits16, true> : beam_select_kernel<Logits16, false>)
                        : (aligned ? beam_select_kernel<Logits32, true> : beam_select_kernel<Logits32, false>);

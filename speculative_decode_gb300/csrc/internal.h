@@ -200,9 +200,10 @@ struct SelectParams {
     float2 *part_sums;        // [B * W][n_chunks] maximum, sum of exp(x - maximum)
     int32_t *counters;        // [B], zero between calls
     int32_t B, W, V, K, eos, n_chunks, chunk;
+    uint32_t by_K, by_W;      // set at launch
 };
 // aligned: every row starts on a 16-byte boundary
-cudaError_t launch_beam_select(const SelectParams &p, bool bf16, bool aligned, cudaStream_t stream);
+cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStream_t stream);
 int beam_select_max_chunk(bool bf16, bool aligned);  // most values of a row for one CTA
 
 struct ReorderParams {
