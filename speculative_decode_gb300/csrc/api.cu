@@ -870,16 +870,20 @@ int check_select(int32_t groups, int32_t width, int32_t vocab, int32_t picks) {
     return SA_OK;
 }
 
-// Chunks of a row: the number whose estimated time is least. In values of a
-// row: a CTA takes its chunk and about 20,000 values' time to pick from it, four
-// of them run on an SM at once, and the merge takes 6,000 for each 1024 picks of a
-// group and 512 a chunk (256 rows of 128256: 2 chunks 28 us, 3 35, 4 32, 7 35).
-int32_t select_cut(int64_t rows, int64_t width, int64_t vocab, int64_t picks, int max_chunk, int sms) {
+// Chunks of a row: the number whose estimated time is least. In cycles: four
+// CTAs run on an SM at once, a round of them starting and ending in 6000; the
+// values pass at the memory's rate, a batch of 4096 (8192) in no less than 1500; each CTA
+// has 2400 cycles of its own work, and the merge 1250 for each 1024 picks
+// of a group. Measured, chunks: 256 fp32 rows of 128256, 2: 27.8 us, 3: 35.0, 4: 32.9,
+// 6: 35.4; 65 bf16 rows of 50257, 2: 13.7 us, 4: 13.1, 9: 14.4.
+int32_t select_cut(int64_t rows, int64_t width, int64_t vocab, int64_t picks, bool bf16, int max_chunk, int sms) {
     const int64_t least = (vocab + max_chunk - 1) / max_chunk, most = std::min(select_chunks(vocab), least + 63);
+    const int64_t batch = max_chunk / beam_select_max_batches();
     int64_t best = INT64_MAX, cut = least;
     for (int64_t n = least; n <= most; ++n) {
-        const int64_t waves = (rows * n + 4 * sms - 1) / (4 * sms);
-        const int64_t cost = waves * ((vocab + n - 1) / n + 20000) + (width * n * picks + 1023) / 1024 * 6000 + n * 512;
+        const int64_t chunk = (vocab + n - 1) / n, ctas = (rows * n + sms - 1) / sms, waves = (ctas + 3) / 4;
+        const int64_t stream = std::max(ctas * chunk * (bf16 ? 11 : 19) / 100, waves * ((chunk + batch - 1) / batch) * 1500);
+        const int64_t cost = waves * 6000 + stream + ctas * 2400 + (width * n * picks + 1023) / 1024 * 1250 + n * 100;
         if (cost < best) {
             best = cost;
             cut = n;
@@ -930,7 +934,7 @@ static int select_impl(const void *logits, bool bf16, int64_t logits_stride, con
     p.K = num_select;
     p.eos = eos_token;
     p.n_chunks = select_cut(static_cast<int64_t>(num_groups) * beam_width, beam_width, vocab, num_select,
-                            beam_select_max_chunk(bf16, rows_aligned), sms);
+                            bf16, beam_select_max_chunk(bf16, rows_aligned), sms);
     p.chunk = ((vocab + p.n_chunks - 1) / p.n_chunks + 7) / 8 * 8;  // even, in 16-byte pieces
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (launch_beam_select(p, bf16, rows_aligned, s) != cudaSuccess) return SA_ERR_CUDA;

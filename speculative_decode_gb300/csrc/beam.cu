@@ -13,12 +13,12 @@
 // Each thread carries its maximum and its sum of exp(x - max), and keeps every
 // batch's maximum in shared memory. The K largest logits are found afterwards (a
 // row's order is its logits' order, so no sum is needed to choose them): each
-// of the eight warps finds its J-th largest lane maximum, J = ceil(K / 8); at
-// least J values of each warp reach the least of those, so the K largest of
-// the chunk do. The batches whose maximum reaches it (about 20 for K = 8) are
-// read again, from the L2, and their values that reach it ranked by counting.
-// When many do (heavy ties) the lowest tokens among the equal ones are taken in
-// order, and otherwise the values one by one as block-wide maxima.
+// of the eight warps gives its four largest lane maxima; the K-th largest of
+// these 32 is reached by K lanes, so by the K largest logits of the chunk, and
+// by few others. The batches whose maximum reaches it are read again, from the L2,
+// and their values that reach it ranked by counting. When many do (heavy ties) the
+// lowest tokens among the equal ones are taken in order, and otherwise the
+// values one by one as block-wide maxima.
 //
 // The last CTA of a group to finish (one atomic counter a group, no spinning)
 // merges the sums into each row's lse and the chunks' picks into the group's.
@@ -48,6 +48,8 @@ constexpr int kCap = 1024;       // collected candidates of a chunk
 constexpr int kRankMost = 128;   // ranked by counting up to this many
 constexpr int kMergeCap = 1024;  // entries of one merge step
 constexpr int kMaxBatches = 16;  // batches of a chunk
+constexpr int kTops = 4;         // largest lane maxima of a warp
+static_assert(kWarps * kTops == 32 && kMaxBeamWidth <= 32, "a lane for each, enough for every K");
 constexpr int kMaxBeams = kMaxBeamWidth;
 constexpr int kIndexBits = 27;   // tokens in a merge key
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
@@ -143,11 +145,21 @@ struct Piece<false> {
 template <typename L, bool kAligned>
 struct Chunk {
     using T = typename L::type;
+    using Pieces = Piece<kAligned>;
     static constexpr int kVec = L::kVec, kLoads = kAligned ? 4 : 2;
     static constexpr int kBatch = kThreads * kLoads * kVec;
     const T *row;
-    int begin, end, vocab;
-    int skew;  // bytes of the row's start behind a 16-byte boundary
+    int begin, end;
+    int skew;        // bytes of the row's start behind a 16-byte boundary
+    int low, high;   // pieces from low to high lie in the chunk, their words in the row
+
+    __device__ __forceinline__ Chunk(const T *row_, int vocab, int begin_, int end_)
+        : row(row_), begin(begin_), end(end_) {
+        constexpr int kBytes = static_cast<int>(sizeof(T));
+        skew = kAligned ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        low = (skew + kBytes - 1) / kBytes;
+        high = kAligned ? end - kVec : min(end - kVec, vocab - (32 - skew + kBytes - 1) / kBytes);
+    }
 
     __device__ __forceinline__ int first(int batch, int i) const {
         return begin + batch * kBatch + (i * kThreads + static_cast<int>(threadIdx.x)) * kVec;
@@ -168,17 +180,15 @@ struct Chunk {
         const int at = first(batch, i);
         Piece<kAligned> p;
         if constexpr (kAligned) {
-            p.a = at + kVec <= end ? *reinterpret_cast<const uint4 *>(row + at) : ends(at);
+            p.a = at <= high ? *reinterpret_cast<const uint4 *>(row + at) : ends(at);
         } else {
-            constexpr int kBytes = static_cast<int>(sizeof(T));
-            // the words lie inside the row, and the values inside the chunk
-            p.end = at * kBytes < skew || at + kVec > end || (vocab - at) * static_cast<int64_t>(kBytes) < 32 - skew;
+            p.end = at < low || at > high;
             if (p.end) {
                 p.a = ends(at);
             } else {
                 const uint4 *word = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + at) - skew);
                 p.a = word[0];
-                if (skew != 0) p.b = word[1];
+                p.b = word[1];
             }
         }
         return p;
@@ -187,7 +197,7 @@ struct Chunk {
     __device__ __forceinline__ void values(const Piece<kAligned> &p, float (&x)[kVec]) const {
         uint4 v = p.a;
         if constexpr (!kAligned) {
-            if (skew != 0 && !p.end) {
+            if (!p.end) {
                 const uint32_t s = (skew & 3) * 8;
                 const uint32_t w[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
                 switch (skew >> 2) {  // the same for the whole CTA
@@ -234,7 +244,7 @@ __device__ __forceinline__ Candidate make_candidate(double value, int beam, uint
 
 struct SelectShared {
     float m[kWarps], s[kWarps];
-    uint32_t tau[kWarps];
+    uint32_t top[kWarps * kTops];
     int n, last, scan[kWarps];
     uint64_t red[2][kWarps];
     int rank[kRankMost];
@@ -286,15 +296,32 @@ __device__ __forceinline__ double log_of_sum(float hi, float lo) {
     return static_cast<double>(k) * 0.69314718055994530942 + (static_cast<double>(2.f * z) + static_cast<double>(small));
 }
 
-// The warp's J-th largest of the lanes' keys (0 where fewer lanes have one).
-__device__ __forceinline__ uint32_t jth_largest(uint32_t key, int J) {
-    uint32_t jth = 0;
-    for (int j = 0; j < J; ++j) {
-        jth = __reduce_max_sync(0xffffffffu, key);
-        const uint32_t who = __ballot_sync(0xffffffffu, key == jth);
-        if (static_cast<int>(threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+// The warp's kTops largest of the lanes' keys to S.top (0 where fewer lanes have one).
+__device__ __forceinline__ void put_tops(SelectShared &S, uint32_t key) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < kTops; ++j) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t who = __ballot_sync(0xffffffffu, key == top);
+        if (lane == j) mine = top;
+        if (lane == __ffs(who) - 1) key = 0;
     }
-    return jth;
+    if (lane < kTops) S.top[warp * kTops + lane] = mine;
+}
+
+// The K-th largest of S.top, one a lane: at least K lanes of the block have a
+// key that reaches it.
+__device__ __forceinline__ uint32_t kth_top(const SelectShared &S, int K) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t mine = S.top[lane];
+    int ahead = 0;
+#pragma unroll
+    for (int o = 0; o < 32; ++o) {
+        const uint32_t other = S.top[o];
+        ahead += other > mine || (other == mine && o < lane);
+    }
+    return __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, ahead == K - 1)) - 1);
 }
 
 // The slots behind the `n` continuations of a value above -inf: continuations
@@ -453,15 +480,12 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
             const float low = value - err;
             if (low > -INFINITY) least = max(least, order32(low));
         }
-        const uint32_t jth = jth_largest(least, (K + kWarps - 1) / kWarps);
-        if (lane == 0) S.tau[warp] = jth;
+        put_tops(S, least);
         if (t == 0) S.n = n;
         if (t < kRankMost) S.rank[t] = 0;
         if (t < n) S.kept[t] = S.best[t];
         __syncthreads();
-        uint32_t tau = S.tau[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
+        const uint32_t tau = kth_top(S, K);
         const float floor = tau <= kOrderNegInf ? -INFINITY : order32_value(tau);
 #pragma unroll
         for (int u = 0; u < kMine; ++u)
@@ -536,44 +560,64 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
 }
 
 // The chunk's K largest values as keys, best first, to out (0: none). tau: the
-// threshold that at least K values reach (0: fewer than K lanes have a value,
-// every value is collected).
-template <typename C, typename L>
+// threshold that at least K values reach (that of -inf or
+// less: fewer than K lanes have a value, every value is collected).
+template <typename C>
 __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, int batches, uint32_t tau, int K,
                                              uint64_t *out) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float at_least = tau <= kOrderNegInf ? -INFINITY : order32_value(tau);
-    // f(x, token) of the thread's values in the batches whose maximum reaches
-    // x_min. The lanes of a warp read their batches, one each, together.
-    auto visit = [&](float x_min, auto &&f) {
+    // f(pieces, batch) of the thread's batches whose maximum reaches the
+    // threshold. The lanes of a warp read their batches, one each, together.
+    using PieceOf = typename C::Pieces;
+    auto visit = [&](auto &&f) {
         uint32_t left = 0;
         for (int b = 0; b < batches; ++b) {
             const float top = S.batch_max[b][t];
-            left |= static_cast<uint32_t>(top >= x_min && top > -INFINITY) << b;
+            left |= static_cast<uint32_t>(top >= at_least && top > -INFINITY) << b;
         }
         while (__any_sync(0xffffffffu, left != 0)) {
             if (left == 0) continue;
             const int b = __ffs(left) - 1;
             left &= left - 1;
-            decltype(chunk.load(0, 0)) v[C::kLoads];
+            PieceOf v[C::kLoads];
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) v[i] = chunk.load(b, i);
+            f(v, b);
+        }
+    };
+    // The values that reach the threshold (or pass it) to S.keys: counted first, so
+    // that a lane asks for its places once.
+    auto collect = [&](bool above) {
+        visit([&](const PieceOf(&v)[C::kLoads], int b) {
+            uint32_t hit = 0;
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) {
+                float x[C::kVec];
+                chunk.values(v[i], x);
+#pragma unroll
+                for (int e = 0; e < C::kVec; ++e)
+                    hit |= static_cast<uint32_t>((above ? x[e] > at_least : x[e] >= at_least) && x[e] > -INFINITY)
+                           << (i * C::kVec + e);
+            }
+            if (hit == 0) return;
+            int to = atomicAdd(&S.n, __popc(hit));
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) {
+                if ((hit >> (i * C::kVec) & ((1u << C::kVec) - 1)) == 0) continue;
                 float x[C::kVec];
                 chunk.values(v[i], x);
                 const int first = chunk.first(b, i);
 #pragma unroll
                 for (int e = 0; e < C::kVec; ++e)
-                    if (x[e] >= x_min && x[e] > -INFINITY) f(x[e], first + e);
+                    if (hit >> (i * C::kVec + e) & 1) {
+                        if (to < kCap) S.keys[to] = pick_key(x[e], first + e);
+                        ++to;
+                    }
             }
-        }
+        });
     };
-    auto collect = [&](float x, int token) {
-        const int to = atomicAdd(&S.n, 1);
-        if (to < kCap) S.keys[to] = pick_key(x, token);
-    };
-    visit(at_least, collect);
+    collect(false);
     __syncthreads();
     int n = S.n;
     if (n > kCap && at_least > -INFINITY) {
@@ -582,9 +626,7 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
         __syncthreads();
         if (t == 0) S.n = 0;
         __syncthreads();
-        visit(at_least, [&](float x, int token) {
-            if (x > at_least) collect(x, token);
-        });
+        collect(true);
         __syncthreads();
         n = S.n;
         if (n <= kCap - kMaxBeams) {
@@ -648,9 +690,17 @@ __device__ __forceinline__ void pick_largest(SelectShared &S, const C &chunk, in
             for (int o = t; o < n; o += kThreads)
                 if (S.keys[o] < last) best = max(best, S.keys[o]);
         } else {
-            visit(at_least, [&](float x, int token) {
-                const uint64_t key = pick_key(x, token);
-                if (key < last) best = max(best, key);
+            visit([&](const PieceOf(&v)[C::kLoads], int b) {
+#pragma unroll
+                for (int i = 0; i < C::kLoads; ++i) {
+                    float x[C::kVec];
+                    chunk.values(v[i], x);
+#pragma unroll
+                    for (int e = 0; e < C::kVec; ++e) {
+                        const uint64_t key = x[e] > -INFINITY ? pick_key(x[e], chunk.first(b, i) + e) : 0;
+                        if (key < last) best = max(best, key);
+                    }
+                }
             });
         }
         best = warp_max(best);
@@ -674,19 +724,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
 
     if (P.finished == nullptr || P.finished[row] == 0) {
         if (t == 0 && chunk_at == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.scores + row));  // for the merge
-        C chunk;
-        chunk.row = static_cast<const typename L::type *>(P.logits) + static_cast<int64_t>(row) * P.stride;
-        chunk.skew = static_cast<int>(reinterpret_cast<uintptr_t>(chunk.row) & 15);
-        chunk.vocab = P.V;
-        chunk.begin = chunk_at * P.chunk;
-        chunk.end = min(P.V, chunk.begin + P.chunk);
+        const int begin = chunk_at * P.chunk;
+        const C chunk(static_cast<const typename L::type *>(P.logits) + static_cast<int64_t>(row) * P.stride, P.V, begin,
+                      min(P.V, begin + P.chunk));
         const int batches = (chunk.end - chunk.begin + C::kBatch - 1) / C::kBatch;  // 0 behind the row
-        decltype(chunk.load(0, 0)) next[C::kLoads];
+        typename C::Pieces next[C::kLoads];
 #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) next[i] = chunk.load(0, i);
         float m = -INFINITY, sum = 0.f;
         for (int b = 0; b < batches; ++b) {
-            decltype(chunk.load(0, 0)) now[C::kLoads];
+            typename C::Pieces now[C::kLoads];
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) now[i] = next[i];
             if (b + 1 < batches) {
@@ -723,18 +770,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
         float warp_sum = m > -INFINITY ? sum * ex2((m - warp_m) * kLog2e) : 0.f;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) warp_sum += __shfl_xor_sync(0xffffffffu, warp_sum, o);
-        const uint32_t jth = jth_largest(key, (P.K + kWarps - 1) / kWarps);
+        put_tops(S, key);
         if (lane == 0) {
             S.m[warp] = warp_m;
             S.s[warp] = warp_sum;
-            S.tau[warp] = jth;
         }
         if (t == 0) S.n = 0;
         if (t < kRankMost) S.rank[t] = 0;
         __syncthreads();
-        uint32_t tau = S.tau[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) tau = min(tau, S.tau[w]);
         const int64_t list = static_cast<int64_t>(row) * P.n_chunks + chunk_at;
         if (t == 0) {
             float top = S.m[0];
@@ -744,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
                 for (int w = 0; w < kWarps; ++w) s += S.s[w] * ex2((S.m[w] - top) * kLog2e);
             P.part_sums[list] = make_float2(top, s);
         }
-        pick_largest<C, L>(S, chunk, batches, tau, P.K, P.part_keys + list * P.K);
+        pick_largest<C>(S, chunk, batches, kth_top(S, P.K), P.K, P.part_keys + list * P.K);
     }
 
     // ---- count this CTA; the last one of a group merges
@@ -822,6 +865,8 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const ReorderPar
 }
 
 }  // namespace
+
+int beam_select_max_batches() { return kMaxBatches; }
 
 int beam_select_max_chunk(bool bf16, bool aligned) {
     return kMaxBatches * (bf16 ? (aligned ? Chunk<Logits16, true>::kBatch : Chunk<Logits16, false>::kBatch)

@@ -204,7 +204,8 @@ struct SelectParams {
 };
 // aligned: every row starts on a 16-byte boundary
 cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStream_t stream);
-int beam_select_max_chunk(bool bf16, bool aligned);  // most values of a row for one CTA
+int beam_select_max_batches();
+int beam_select_max_chunk(bool bf16, bool aligned);  // most values of a row for one CTA, that many batches
 
 struct ReorderParams {
     const int32_t *parents, *table, *seq_lens;
