@@ -34,6 +34,7 @@
 // those of the k-th beam that has no child (there are as many), into which the
 // parent's rows of the unfilled page are copied. Nothing that is read is
 // written, so one kernel does it in any order. Bound: bytes copied.
+#include <algorithm>
 #include <cfloat>
 
 #include "common.cuh"
@@ -245,7 +246,7 @@ __device__ __forceinline__ Candidate make_candidate(double value, int beam, uint
 struct SelectShared {
     float m[kWarps], s[kWarps];
     uint32_t top[kWarps * kTops];
-    int n, last, scan[kWarps];
+    int n, last, more, scan[kWarps];
     uint64_t red[2][kWarps];
     int rank[kRankMost];
     float batch_max[kMaxBatches][kThreads];
@@ -379,31 +380,35 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int row0 = g * P.W;
     const unsigned W = P.W, n_chunks = P.n_chunks, K = P.K;
-    // Entries in steps of kMergeCap, the best of the steps before kept. They are
-    // the lists' in turn, consecutive lists of different rows, shifted from chunk
-    // to chunk; entry 8 q + r of a step goes to lane q of warp (q + r) % 8. So every
-    // warp sees the best of all rows, however many there are. The first step's
+    // Entries in steps of kMergeCap, the best of the steps before kept: R ranks
+    // of all lists, then the next R, until no list's last one may still matter.
+    // They are the lists' in turn, consecutive lists of different rows, shifted from
+    // chunk to chunk; entry 8 q + r of a step goes to lane q of warp (q + r) % 8. So
+    // every warp sees the best of all rows, however many there are. The first step's
     // keys are loaded while the sums are merged.
-    const unsigned total = W * n_chunks * K;
-    auto place = [&](unsigned e, unsigned &w, unsigned &list_at) {
-        const unsigned list = __umulhi(e, P.by_K) + (K == 1 ? e : 0), chunk = __umulhi(list, P.by_W) + (W == 1 ? list : 0);
+    const unsigned lists = W * n_chunks, R = P.R;
+    auto place = [&](unsigned e, unsigned rank0, unsigned &w, unsigned &chunk, unsigned &rank) {
+        const unsigned list = __umulhi(e, P.by_R) + (R == 1 ? e : 0);
+        chunk = __umulhi(list, P.by_W) + (W == 1 ? list : 0);
         const unsigned turn = list - chunk * W + chunk;
         w = turn - (__umulhi(turn, P.by_W) + (W == 1 ? turn : 0)) * W;
-        list_at = chunk * K + (e - list * K);
+        rank = rank0 + (e - list * R);
     };
     auto entry_of = [&](int u) {
         const unsigned q = u * 32 + lane;
         return 8 * q + ((warp - q) & 7);
     };
-    auto key_of = [&](unsigned e) {
-        unsigned w, list_at;
-        place(e, w, list_at);
-        return __ldcg(P.part_keys + static_cast<int64_t>(row0 + w) * n_chunks * K + list_at);
+    auto key_of = [&](unsigned w, unsigned chunk, unsigned rank) {
+        return rank < K ? __ldcg(P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + chunk) * K + rank) : 0;
     };
     constexpr int kMine = kMergeCap / kThreads;
     uint64_t mine[kMine];
 #pragma unroll
-    for (int u = 0; u < kMine; ++u) mine[u] = entry_of(u) < total ? key_of(entry_of(u)) : 0;
+    for (int u = 0; u < kMine; ++u) {
+        unsigned w, chunk, rank;
+        place(entry_of(u), 0, w, chunk, rank);
+        mine[u] = entry_of(u) < lists * R ? key_of(w, chunk, rank) : 0;
+    }
     if (t < P.W) {
         S.score[t] = P.scores[row0 + t];
         S.done[t] = P.finished != nullptr && P.finished[row0 + t] != 0;
@@ -448,24 +453,30 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
                               ~static_cast<uint32_t>(key));
     };
     int n = 0;
-    for (unsigned e0 = 0; e0 < total; e0 += kMergeCap) {
+    if (t == 0) S.more = 0;
+    for (unsigned rank0 = 0, e0 = 0; rank0 < K;) {
         // The values in 32 bits, with bounds on their errors, leave few to be
         // computed in 64: those that may reach what K values surely reach.
         float most[kMine];
         uint32_t least = 0;
         unsigned of[kMine];
+        bool last_rank[kMine];
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
             const unsigned e = e0 + entry_of(u);
+            unsigned w, chunk, rank;
+            place(e, rank0, w, chunk, rank);
             most[u] = -INFINITY;
             of[u] = 0;
-            if (e0 > 0) mine[u] = e < total ? key_of(e) : 0;
-            if (e >= total) continue;
-            unsigned w, list_at;
-            place(e, w, list_at);
+            last_rank[u] = rank == rank0 + R - 1;
+            if (e >= lists * R) {
+                mine[u] = 0;
+                continue;
+            }
+            if (rank0 + e0 > 0) mine[u] = key_of(w, chunk, rank);
             of[u] = w;
             const float score = S.score[w];
-            if (S.done[w]) mine[u] = list_at == 0 ? 1 : 0;
+            if (S.done[w]) mine[u] = chunk == 0 && rank == 0 ? 1 : 0;
             if (mine[u] == 0 || !(score > -INFINITY)) {
                 mine[u] = 0;
                 continue;
@@ -490,6 +501,7 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
 #pragma unroll
         for (int u = 0; u < kMine; ++u)
             if (mine[u] != 0 && !(most[u] < floor)) {
+                if (last_rank[u]) S.more = 1;
                 const int at = atomicAdd(&S.n, 1);
                 if (at < kRankMost) {
                     S.keys[at] = mine[u];
@@ -537,6 +549,14 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
             n = static_cast<int>(K);  // more than K entries have a value
         }
         __syncthreads();
+        e0 += kMergeCap;
+        if (e0 >= lists * R) {  // these ranks are done
+            if (S.more == 0) break;
+            __syncthreads();
+            if (t == 0) S.more = 0;
+            e0 = 0;
+            rank0 += R;
+        }
     }
     if (t < n) {
         const Candidate c = S.best[t];
@@ -875,7 +895,8 @@ int beam_select_max_chunk(bool bf16, bool aligned) {
 
 cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStream_t stream) {
     // quotients of up to 2^27 as the upper half of a product: exact for divisors up to 32
-    p.by_K = static_cast<uint32_t>(((1ull << 32) + p.K - 1) / p.K);
+    p.R = static_cast<uint32_t>(std::max(1, std::min(p.K, kMergeCap / (p.W * p.n_chunks))));
+    p.by_R = static_cast<uint32_t>(((1ull << 32) + p.R - 1) / p.R);
     p.by_W = static_cast<uint32_t>(((1ull << 32) + p.W - 1) / p.W);
     const int64_t ctas = static_cast<int64_t>(p.B) * p.W * p.n_chunks;
     auto kernel = bf16 ? (aligned ? beam_select_kernel<Logits16, true> : beam_select_kernel<Logits16, false>)

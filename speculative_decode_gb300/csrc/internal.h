@@ -200,7 +200,7 @@ struct SelectParams {
     float2 *part_sums;        // [B * W][n_chunks] maximum, sum of exp(x - maximum)
     int32_t *counters;        // [B], zero between calls
     int32_t B, W, V, K, eos, n_chunks, chunk;
-    uint32_t by_K, by_W;      // set at launch
+    uint32_t R, by_R, by_W;   // ranks of a merge step, and divisors; set at launch
 };
 // aligned: every row starts on a 16-byte boundary
 cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStream_t stream);

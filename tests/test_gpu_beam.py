@@ -155,6 +155,49 @@ def test_select_of_sorted_and_striped_rows():
         check_select(x, s, K, gap=False, offset=1)
 
 
+def test_select_where_one_part_of_one_beam_gives_everything():
+    """All picks stand together in one beam's row; the other beams are far behind."""
+    for V, W in ((40000, 32), (128256, 16), (3000, 32)):
+        up = torch.arange(V, dtype=torch.float32) / 100
+        x = torch.stack([up.roll(7 * w) for w in range(W)])[None]
+        s = np.full((1, W), -5000.0)
+        s[0, W // 2] = -1.0
+        check_select(x, s, 32, gap=False)
+        s[0, 1] = -1.0 - 2.0 ** -7                # and two that interleave
+        check_select(x, s, 32, gap=False)
+
+
+@pytest.mark.parametrize("B,W,V,K,dtype", [(1, 2, 1 << 26, 32, torch.float32), (1, 32, 1 << 22, 32, torch.bfloat16),
+                                           (16384, 1, 64, 3, torch.float32)])
+def test_select_of_the_largest_sizes(B, W, V, K, dtype):
+    """Against torch in 64 bits on the GPU (rows with no ties at the border)."""
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(B, W, V, generator=gen, device="cuda").mul_(3)
+    spots = torch.randint(0, V, (B, W, 40), generator=gen, device="cuda")
+    if V > 64:
+        x.scatter_reduce_(2, spots, torch.rand(B, W, 40, generator=gen, device="cuda") * 16 + 20, "amax")
+    x = x.to(dtype)
+    s = -torch.rand(B, W, generator=gen, device="cuda")
+    best, tokens = x.double().topk(K, -1)
+    lse = torch.stack([row.double().logsumexp(-1) for row in x.flatten(0, 1)]).view(B, W, 1) if V > 64 else x.double().logsumexp(-1, keepdim=True)
+    value = (s.double()[..., None] + (best - lse)).flatten(1)
+    v, at = value.topk(K, -1)
+    ws = torch.zeros(sa.beam_select_workspace_size(B, W, V, K), dtype=torch.uint8, device="cuda")
+    tok, par = (torch.zeros(B, K, dtype=torch.int32, device="cuda") for _ in range(2))
+    sc = torch.zeros(B, K, device="cuda")
+    sa.beam_select(x, s, tok, par, sc, ws)
+    torch.cuda.synchronize()
+    assert ((sc.double() - v).abs() <= 2.0 ** -24 * v.abs() + SUM).all()
+    # where the values are apart, the picks are the same; equal bf16 logits may
+    # come from topk in any order
+    apart = torch.ones_like(v, dtype=torch.bool)
+    apart[:, 1:] &= v[:, :-1] - v[:, 1:] > GAP
+    apart[:, :-1] &= v[:, :-1] - v[:, 1:] > GAP
+    apart[:, -1] = False
+    assert apart[:, :-1].any()
+    assert (par == at // K)[apart].all() and (tok == tokens.flatten(1).gather(1, at))[apart].all()
+
+
 def test_select_of_infinite_and_odd_values():
     x, s, _ = draws(11, 2, 4, 6000)
     x[0, 0, 17] = float("inf")
