@@ -425,7 +425,7 @@ typedef struct {
     const float *inv_freq; /* device fp32 [rotary_dim / 2] */
     const float *q_weight; /* device fp32 [128], 16-byte aligned, or NULL: queries have no norm */
     const float *k_weight; /* the same for keys */
-    float eps;             /* in (0, 1]; read when there is a weight */
+    float eps;             /* a normal number up to 1; read when there is a weight */
     int32_t rotary_dim;    /* R: 0 (no rotation) or a multiple of 16 up to 128 */
     int32_t interleaved;
 } sa_rope;

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -681,7 +682,7 @@ int check_rope(const sa_rope *r, int head_dim) {
     if (r->rotary_dim < 0 || r->rotary_dim > kHeadDim || r->rotary_dim % 2 != 0) return SA_ERR_ARG;
     if (r->rotary_dim % 16 != 0) return SA_ERR_UNSUPPORTED;
     if (r->rotary_dim > 0 && r->inv_freq == nullptr) return SA_ERR_ARG;
-    if ((r->q_weight != nullptr || r->k_weight != nullptr) && !(r->eps > 0.f && r->eps <= 1.f)) return SA_ERR_ARG;
+    if ((r->q_weight != nullptr || r->k_weight != nullptr) && !(r->eps >= FLT_MIN && r->eps <= 1.f)) return SA_ERR_ARG;
     if (!aligned(r->inv_freq, 4) || !aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return SA_ERR_ARG;
     return SA_OK;
 }

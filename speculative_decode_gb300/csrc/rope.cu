@@ -10,15 +10,16 @@
 // int4 page rows). t is formed in 64 bits, as a fraction of a turn: at
 // position 10^6 a 32-bit product would be off by up to 0.06 rad.
 //
-// Half a warp holds a row, a lane eight of its values: four first and four
+// Eight lanes hold a row, a lane sixteen of its values: eight first and eight
 // second values of pairs where it is rotated, so a rotation stays in the lane.
 // With the angles and the weights the row's values A, B of the pairs become
-// r (A wc - B ws), r (A ws' + B wc'), four products prepared once a token: about
-// 60 instructions a pair of rows, in packed 32-bit arithmetic. A warp takes one
-// token, or every `parts`-th group of a token's rows; the next group's loads
-// are in flight while one is turned. Bound: bytes moved (a row in, a row out)
-// for many tokens, two dependent memory round trips (lengths, then rows) for
-// few.
+// r (A wc - B ws), r (A ws' + B wc'); the four products are made once a token and
+// kept in shared memory. A warp turns four rows at a time, in packed 32-bit
+// arithmetic, about a hundred instructions. It takes one token, or every
+// `parts`-th four rows of one; the loads go through a ring in shared memory
+// (asynchronous copies, each lane its own bytes, so no barrier), four steps
+// ahead. Bound: bytes moved (a row in, a row out) for many tokens, two
+// dependent memory round trips (lengths, then rows) for few.
 #include <cfloat>
 
 #include "common.cuh"
@@ -29,17 +30,19 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroup = 2;  // row pairs of a group: two of queries, or one of keys and one of values
+constexpr int kAhead = 4;    // steps of four rows in flight per warp
+constexpr int kResident = 8; // CTAs per SM
 
-__device__ __forceinline__ float half_warp_sum(float v, uint32_t mask) {
+// Sum and maximum over a row's eight lanes.
+__device__ __forceinline__ float row_sum(float v, uint32_t mask) {
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+    for (int o = 4; o >= 1; o >>= 1) v += __shfl_xor_sync(mask, v, o);
     return v;
 }
 
-__device__ __forceinline__ float half_warp_max(float v, uint32_t mask) {
+__device__ __forceinline__ float row_max(float v, uint32_t mask) {
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
+    for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
 }
 
@@ -65,90 +68,117 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// A lane's eight values of a row: A[0..1] are the first values of its pairs
-// (two in each), B[0..1] the second.
-struct Eight {
-    uint64_t A[2], B[2];
+// A lane's values of a row: A holds the first values of its eight pairs (two in
+// each), B the second.
+struct Values {
+    uint64_t A[4], B[4];
 };
 
-template <bool kInterleaved>
-__device__ __forceinline__ Eight unpack(uint2 a, uint2 b) {
-    if constexpr (kInterleaved)
-        return Eight{{two(bf16_lo(a.x), bf16_lo(a.y)), two(bf16_lo(b.x), bf16_lo(b.y))},
-                     {two(bf16_hi(a.x), bf16_hi(a.y)), two(bf16_hi(b.x), bf16_hi(b.y))}};
-    else
-        return Eight{{two(bf16_lo(a.x), bf16_hi(a.x)), two(bf16_lo(a.y), bf16_hi(a.y))},
-                     {two(bf16_lo(b.x), bf16_hi(b.x)), two(bf16_lo(b.y), bf16_hi(b.y))}};
-}
-
-// Its values as they stand in memory: four at the lane's first place, four at
-// its second.
-template <bool kInterleaved>
-__device__ __forceinline__ void in_order(const Eight &v, float (&y)[8]) {
-    const float2 a0 = apart(v.A[0]), a1 = apart(v.A[1]), b0 = apart(v.B[0]), b1 = apart(v.B[1]);
-    if constexpr (kInterleaved) {
-        y[0] = a0.x, y[1] = b0.x, y[2] = a0.y, y[3] = b0.y;
-        y[4] = a1.x, y[5] = b1.x, y[6] = a1.y, y[7] = b1.y;
-    } else {
-        y[0] = a0.x, y[1] = a0.y, y[2] = a1.x, y[3] = a1.y;
-        y[4] = b0.x, y[5] = b0.y, y[6] = b1.x, y[7] = b1.y;
+__device__ __forceinline__ void unpack(const uint4 &a, const uint4 &b, bool interleaved, Values &v) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (interleaved) {
+            v.A[i] = two(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+            v.B[i] = two(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+        } else {
+            v.A[i] = two(bf16_lo(w[i]), bf16_hi(w[i]));
+            v.B[i] = two(bf16_lo(w[4 + i]), bf16_hi(w[4 + i]));
+        }
     }
 }
 
-// What a lane's values are multiplied with, the row's factor aside: A' = A ac -
-// B bs, B' = A as + B bc with the weights in them; a lane that is not rotated
-// takes A ac and B bc.
-struct Turn {
-    uint64_t ac[2], bs[2], as[2], bc[2];  // bs with its sign
-};
+// The values as they stand in memory: eight at the lane's first place, eight at
+// its second.
+__device__ __forceinline__ void in_order(const Values &v, bool interleaved, float (&y)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = apart(v.A[i]), b = apart(v.B[i]);
+        if (interleaved) {
+            y[4 * i] = a.x, y[4 * i + 1] = b.x, y[4 * i + 2] = a.y, y[4 * i + 3] = b.y;
+        } else {
+            y[2 * i] = a.x, y[2 * i + 1] = a.y, y[8 + 2 * i] = b.x, y[8 + 2 * i + 1] = b.y;
+        }
+    }
+}
 
-// The factor rsqrt(mean(x^2) + eps) of the half warp's row. A sum of squares
-// past 32 bits is formed again of scaled values (a power of two), so rows of
-// any finite values have their norm.
-__device__ __forceinline__ float norm_factor(Eight &v, float eps, uint32_t mask) {
+// The factor rsqrt(mean(x^2) + eps) of a row. A sum of squares past 32 bits is
+// formed again of scaled values (a power of two), so rows of any finite values
+// have their norm. eps is a normal number, so the flush to zero takes nothing.
+__device__ __forceinline__ float rsqrt_ftz(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float norm_factor(Values &v, float eps, uint32_t mask) {
     auto squares = [&] {
-        uint64_t q = mul2(v.A[0], v.A[0]);
-        q = fma2(v.A[1], v.A[1], q);
-        q = fma2(v.B[0], v.B[0], q);
-        q = fma2(v.B[1], v.B[1], q);
-        const float2 p = apart(q);
-        return half_warp_sum(p.x + p.y, mask);
+        uint64_t p = mul2(v.A[0], v.A[0]), q = mul2(v.B[0], v.B[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            p = fma2(v.A[i], v.A[i], p);
+            q = fma2(v.B[i], v.B[i], q);
+        }
+        const float2 a = apart(p), b = apart(q);
+        return row_sum((a.x + a.y) + (b.x + b.y), mask);
     };
     const float ss = squares();
-    float r = rsqrtf(fmaf(ss, 1.f / kHeadDim, eps));
+    float r = rsqrt_ftz(fmaf(ss, 1.f / kHeadDim, eps));
     if (!(ss <= FLT_MAX)) {
         const uint64_t down = two(0x1p-70f, 0x1p-70f);
-        v = Eight{{mul2(v.A[0], down), mul2(v.A[1], down)}, {mul2(v.B[0], down), mul2(v.B[1], down)}};
-        r = rsqrtf(squares() * (1.f / kHeadDim));  // eps is far below such a row's mean
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v.A[i] = mul2(v.A[i], down);
+            v.B[i] = mul2(v.B[i], down);
+        }
+        r = rsqrt_ftz(squares() * (1.f / kHeadDim));  // eps is far below such a row's mean
     }
     return r;
 }
 
-// The page format of the quantising appends (see kv_append.cu), half a warp a
-// row: scale = amax / Cmax and code = round-half-even(y / scale), both by IEEE
-// division. The lane's values stand at a .. a + 3 and b .. b + 3.
+// The page format of the quantising appends (see kv_append.cu): scale = amax /
+// Cmax and code = round-half-even(y / scale), both by IEEE division. The
+// quotient is taken as a product first, which is off by less than 127 * 2^-21;
+// only where that may change the code is it divided. The lane's values stand at
+// a .. a + 7 and b .. b + 7.
 template <int KB>
-__device__ __forceinline__ void store_codes(const float (&y)[8], int l, int a, int b, uint32_t mask, uint8_t *codes,
+__device__ __forceinline__ void store_codes(const float (&y)[16], int l, int a, int b, uint32_t mask, uint8_t *codes,
                                             float *scale) {
     constexpr int kMax = KB == 8 ? 127 : 7;
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
-    amax = half_warp_max(amax, mask);
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(y[e]));
+    amax = row_max(amax, mask);
     const float sc = __fdiv_rn(amax, static_cast<float>(kMax));
-    uint32_t packed[2] = {0, 0};
+    const bool plain = sc > 1e-30f;
+    const float inv = plain ? __frcp_rn(sc) : 0.f;
+    int c[16];
+    uint32_t unsure = plain ? 0u : 0xffffu;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int c = sc > 0.f ? max(-kMax, min(kMax, __float2int_rn(__fdiv_rn(y[e], sc)))) : 0;
-        if constexpr (KB == 8) packed[e / 4] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (e & 3));
-        else packed[e / 4] |= static_cast<uint32_t>(c + 8) << (4 * (e & 3));
+    for (int e = 0; e < 16; ++e) {
+        const float q = y[e] * inv;
+        c[e] = __float2int_rn(q);
+        const float off = fabsf(q - static_cast<float>(c[e]));
+        unsure |= static_cast<uint32_t>(fabsf(off - 0.5f) < 1e-3f) << e;
+    }
+    if (unsure != 0) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (unsure >> e & 1) c[e] = sc > 0.f ? __float2int_rn(__fdiv_rn(y[e], sc)) : 0;
+    }
+    uint32_t packed[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int k = max(-kMax, min(kMax, c[e]));
+        if constexpr (KB == 8) packed[e / 4] |= (static_cast<uint32_t>(k) & 0xffu) << (8 * (e & 3));
+        else packed[e / 8] |= static_cast<uint32_t>(k + 8) << (4 * (e & 7));
     }
     if constexpr (KB == 8) {
-        *reinterpret_cast<uint32_t *>(codes + a) = packed[0];
-        *reinterpret_cast<uint32_t *>(codes + b) = packed[1];
+        *reinterpret_cast<uint2 *>(codes + a) = make_uint2(packed[0], packed[1]);
+        *reinterpret_cast<uint2 *>(codes + b) = make_uint2(packed[2], packed[3]);
     } else {
-        *reinterpret_cast<uint16_t *>(codes + a / 2) = static_cast<uint16_t>(packed[0]);
-        *reinterpret_cast<uint16_t *>(codes + b / 2) = static_cast<uint16_t>(packed[1]);
+        *reinterpret_cast<uint32_t *>(codes + a / 2) = packed[0];
+        *reinterpret_cast<uint32_t *>(codes + b / 2) = packed[1];
     }
     if (l == 0) *scale = sc;
 }
@@ -206,14 +236,17 @@ __device__ __forceinline__ void locate(const RopeParams &P, int token, TokenPlac
 
 // KB: 0 for dense keys (no pages), 16 for bf16 pages, 8 or 4 for code pages.
 template <int KB, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams P) {
-    __shared__ __align__(16) float s_cos[kWarps][kHeadDim / 2], s_sin[kWarps][kHeadDim / 2];
+__global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeParams P) {
+    __shared__ uint4 s_ring[kWarps][kAhead][2][32];
+    // a lane's products: 8 pairs of A wc, -B ws, A ws, B wc as two runs of four
+    __shared__ __align__(16) float s_mul[kWarps][4][kHeadDim / 2];
+    __shared__ float s_cos[kWarps][kHeadDim / 2], s_sin[kWarps][kHeadDim / 2];
     // the attention kernel that follows reads q and the pages only after this
     // grid has completed
     if constexpr (KB != 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane & 15, side = lane >> 4;
-    const uint32_t mask = 0xffffu << (lane & 16);
+    const int l = lane & 7, side = lane >> 3;
+    const uint32_t mask = 0xffu << (lane & 24);
     const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int parts = 1 << P.parts_log2;
     const int token = static_cast<int>(gw >> P.parts_log2);
@@ -241,44 +274,31 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams P) {
         if (P.positions != nullptr) pos = P.positions[token];
     }
 
-    // where the lane's values stand in a row: the pairs' first and second values
-    // (half a rotation apart, or neighbours), behind them eight in a row
-    const bool rot = l < P.half / 4;
-    const int off_a = kInterleaved || !rot ? 8 * l : 4 * l;
-    const int off_b = kInterleaved || !rot ? off_a + 4 : P.half + 4 * l;
-    // groups of row pairs: the queries', then the keys' with the values'
-    const int nq = (P.Hq + 1) / 2, nk = (P.Hkv + 1) / 2;
-    const int gq = (nq + kGroup - 1) / kGroup;
-    constexpr int kKeys = KB == 0 ? kGroup : kGroup / 2;  // key pairs of a group
-    const int groups = gq + (nk + kKeys - 1) / kKeys;
+    // where the lane's values stand in a row: its pairs' first and second values
+    // (half a rotation apart), or sixteen in a row
+    const bool rot = l < P.half / 8;
+    const int off_a = kInterleaved || !rot ? 16 * l : 8 * l;
+    const int off_b = kInterleaved || !rot ? off_a + 8 : P.half + 8 * l;
+    // steps of four rows: the queries', the keys', the values'
+    const int nq = (P.Hq + 3) / 4, nk = (P.Hkv + 3) / 4;
+    const int steps = nq + (KB == 0 ? nk : 2 * nk);
     const uint16_t *q = P.q + token * P.q_stride + side * kHeadDim;
-    const uint16_t *k = P.k + token * P.k_stride + side * kHeadDim;
-    const uint16_t *v = KB == 0 ? nullptr : P.v + token * P.v_stride + side * kHeadDim;
-    // the head of a group's u-th row, and whether the row is there (a whole half warp)
-    auto head_of = [&](int g, int u) {
-        return 2 * (g < gq ? g * kGroup + u : (g - gq) * kKeys + (u & (kKeys - 1))) + side;
-    };
-    uint2 ra[kGroup], rb[kGroup];
-    auto load = [&](int g, uint2 (&a)[kGroup], uint2 (&b)[kGroup]) {
-        const int heads = g < gq ? P.Hq : P.Hkv;
-#pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            const int h = head_of(g, u);
-            const uint16_t *src = (g < gq ? q : u < kKeys ? k : v) + (h - side) * kHeadDim;
-            a[u] = b[u] = make_uint2(0, 0);
-            if (g < groups && h < heads) {
-                if constexpr (kInterleaved) {
-                    const uint4 r = *reinterpret_cast<const uint4 *>(src + off_a);
-                    a[u] = make_uint2(r.x, r.y);
-                    b[u] = make_uint2(r.z, r.w);
-                } else {
-                    a[u] = *reinterpret_cast<const uint2 *>(src + off_a);
-                    b[u] = *reinterpret_cast<const uint2 *>(src + off_b);
-                }
-            }
+    const uint16_t *k = P.k + token * P.k_stride + (side - 4 * nq) * kHeadDim;
+    const uint16_t *v = P.v + token * P.v_stride + (side - 4 * (nq + nk)) * kHeadDim;
+    // the row of the lanes in a step: 0 queries, 1 keys, 2 values; whether it is there
+    auto kind_of = [&](int i) { return i < nq ? 0 : i < nq + nk ? 1 : 2; };
+    auto head_of = [&](int i, int kind) { return 4 * (i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + side; };
+    auto fetch = [&](int i, int at) {
+        const int kind = kind_of(i);
+        if (i < steps && head_of(i, kind) < (kind == 0 ? P.Hq : P.Hkv)) {
+            const uint16_t *src = (kind == 0 ? q : kind == 1 ? k : v) + i * (4 * kHeadDim);
+            cp_async16(&s_ring[warp][at][0][lane], src + off_a);
+            cp_async16(&s_ring[warp][at][1][lane], src + off_b);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load(part, ra, rb);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(part + a * parts, a);
 
     // the token's angles, while the first rows are on their way
     auto angle = [&](float freq, int j) {
@@ -288,106 +308,102 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams P) {
     if (lane < P.half) angle(freq0, lane);
     if (lane + 32 < P.half) angle(freq1, lane + 32);
     __syncwarp();
-    Turn T;
+    // a kind's products: pair e of lane n's values, two pairs a lane
     auto prepare = [&](const float *weight) {
-        float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
-        if (weight != nullptr) {
-            wa = __ldg(reinterpret_cast<const float4 *>(weight + off_a));
-            wb = __ldg(reinterpret_cast<const float4 *>(weight + off_b));
-        }
-        const uint64_t A[2] = {kInterleaved ? two(wa.x, wa.z) : two(wa.x, wa.y), kInterleaved ? two(wb.x, wb.z) : two(wa.z, wa.w)};
-        const uint64_t B[2] = {kInterleaved ? two(wa.y, wa.w) : two(wb.x, wb.y), kInterleaved ? two(wb.y, wb.w) : two(wb.z, wb.w)};
-        float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (rot) {
-            c = *reinterpret_cast<const float4 *>(&s_cos[warp][4 * l]);
-            s = *reinterpret_cast<const float4 *>(&s_sin[warp][4 * l]);
-        }
-        const uint64_t C[2] = {two(c.x, c.y), two(c.z, c.w)}, S[2] = {two(s.x, s.y), two(s.z, s.w)};
-        const uint64_t minus = two(-1.f, -1.f);
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            T.ac[i] = mul2(A[i], C[i]);
-            T.as[i] = mul2(A[i], S[i]);
-            T.bc[i] = mul2(B[i], C[i]);
-            T.bs[i] = mul2(mul2(B[i], S[i]), minus);
+        for (int h = 0; h < 2; ++h) {
+            const int j = lane + 32 * h, n = j >> 3, e = j & 7;
+            const bool turns = j < P.half;
+            const int pa = kInterleaved ? 2 * j : turns ? j : 16 * n + e;
+            const int pb = kInterleaved ? pa + 1 : turns ? j + P.half : pa + 8;
+            const float wa = weight != nullptr ? weight[pa] : 1.f, wb = weight != nullptr ? weight[pb] : 1.f;
+            const float c = turns ? s_cos[warp][j] : 1.f, s = turns ? s_sin[warp][j] : 0.f;
+            const int at = (e >> 2) * 32 + n * 4 + (e & 3);
+            s_mul[warp][0][at] = wa * c;
+            s_mul[warp][1][at] = -wb * s;
+            s_mul[warp][2][at] = wa * s;
+            s_mul[warp][3][at] = wb * c;
         }
+        __syncwarp();
     };
-    int prepared = -1;
-    for (int g = part; g < groups; g += parts) {
-        uint2 na[kGroup], nb[kGroup];
-        load(g + parts, na, nb);
-        const bool queries = g < gq;
-        const float *weight = queries ? P.q_weight : P.k_weight;
-        if (prepared != static_cast<int>(queries)) {
+    auto product = [&](int which, int i) {  // the products of pairs 2 i, 2 i + 1
+        return *reinterpret_cast<const uint64_t *>(&s_mul[warp][which][(i >> 1) * 32 + l * 4 + (i & 1) * 2]);
+    };
+    int prepared = -1, at = 0;
+    for (int i = part; i < steps; i += parts) {
+        const int kind = kind_of(i), head = head_of(i, kind);
+        const float *weight = kind == 0 ? P.q_weight : P.k_weight;
+        if (kind != 2 && kind != prepared) {
             prepare(weight);
-            prepared = queries;
+            prepared = kind;
         }
-        const int heads = queries ? P.Hq : P.Hkv;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        uint4 a = s_ring[warp][at][0][lane], b = s_ring[warp][at][1][lane];
+        fetch(i + kAhead * parts, at);
+        at = at + 1 == kAhead ? 0 : at + 1;
+        const bool here = head < (kind == 0 ? P.Hq : P.Hkv);  // all the row's lanes
+        float y[16];
+        if (kind != 2) {
+            Values x;
+            unpack(a, b, kInterleaved, x);
+            const float r = weight != nullptr ? norm_factor(x, P.eps, mask) : 1.f;
+            const uint64_t rr = two(r, r);
+            if (rot) {
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            const int head = head_of(g, u);
-            const bool value = !queries && u >= kKeys;
-            uint2 oa = ra[u], ob = rb[u];
-            float y[8];
-            if (!value) {
-                Eight x = unpack<kInterleaved>(ra[u], rb[u]);
-                const float r = weight != nullptr ? norm_factor(x, P.eps, mask) : 1.f;
-                if (rot) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint64_t A = fma2(x.A[i], T.ac[i], mul2(x.B[i], T.bs[i]));
-                        x.B[i] = fma2(x.A[i], T.as[i], mul2(x.B[i], T.bc[i]));
-                        x.A[i] = A;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        x.A[i] = mul2(x.A[i], T.ac[i]);
-                        x.B[i] = mul2(x.B[i], T.bc[i]);
-                    }
+                for (int p = 0; p < 4; ++p) {
+                    const uint64_t A = fma2(x.A[p], product(0, p), mul2(x.B[p], product(1, p)));
+                    const uint64_t B = fma2(x.A[p], product(2, p), mul2(x.B[p], product(3, p)));
+                    x.A[p] = mul2(A, rr);
+                    x.B[p] = mul2(B, rr);
                 }
-                const uint64_t rr = two(r, r);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    x.A[i] = mul2(x.A[i], rr);
-                    x.B[i] = mul2(x.B[i], rr);
-                }
-                in_order<kInterleaved>(x, y);
-                oa = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                ob = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            } else if constexpr (KB == 8 || KB == 4) {
-                y[0] = bf16_lo(oa.x), y[1] = bf16_hi(oa.x), y[2] = bf16_lo(oa.y), y[3] = bf16_hi(oa.y);
-                y[4] = bf16_lo(ob.x), y[5] = bf16_hi(ob.x), y[6] = bf16_lo(ob.y), y[7] = bf16_hi(ob.y);
-            }
-            auto store_row = [&](uint16_t *row) {
-                if constexpr (kInterleaved) {
-                    *reinterpret_cast<uint4 *>(row + off_a) = make_uint4(oa.x, oa.y, ob.x, ob.y);
-                } else {
-                    *reinterpret_cast<uint2 *>(row + off_a) = oa;
-                    *reinterpret_cast<uint2 *>(row + off_b) = ob;
-                }
-            };
-            if (head >= heads) continue;
-            if (queries) {
-                store_row(P.q_out + token * P.q_out_stride + head * kHeadDim);
-            } else if constexpr (KB == 0) {
-                store_row(P.k_out + token * P.k_out_stride + head * kHeadDim);
-            } else if (pid < 0 || pid >= P.num_pages) {
-                if (l == 0) flag_error(P.err, kErrBitPageOOB);
             } else {
-                const int64_t prow = (static_cast<int64_t>(pid) * P.Hkv + head) * kPageSize + slot;
-                if constexpr (KB == 16) {
-                    store_row((value ? P.v_pages : P.k_pages) + prow * kHeadDim);
-                } else {
-                    constexpr int kCodeRow = kHeadDim * KB / 8;
-                    store_codes<KB>(y, l, off_a, off_b, mask, (value ? P.v_codes : P.k_codes) + prow * kCodeRow,
-                                    (value ? P.v_scales : P.k_scales) + prow);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    x.A[p] = mul2(mul2(x.A[p], product(0, p)), rr);
+                    x.B[p] = mul2(mul2(x.B[p], product(3, p)), rr);
                 }
             }
-        }
+            in_order(x, kInterleaved, y);
+            if (KB == 0 || KB == 16 || kind == 0) {
+                a = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                               pack_bf16x2(y[6], y[7]));
+                b = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
+                               pack_bf16x2(y[14], y[15]));
+            }
+        } else if constexpr (KB == 8 || KB == 4) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) ra[u] = na[u], rb[u] = nb[u];
+            for (int e = 0; e < 8; ++e) {
+                y[2 * e] = bf16_lo(w[e]);
+                y[2 * e + 1] = bf16_hi(w[e]);
+            }
+        }
+        if (!here) continue;
+        uint16_t *dst = nullptr;
+        if (kind == 0) {
+            dst = P.q_out + token * P.q_out_stride + head * kHeadDim;
+        } else if constexpr (KB == 0) {
+            dst = P.k_out + token * P.k_out_stride + head * kHeadDim;
+        } else {
+            if (pid < 0 || pid >= P.num_pages) {
+                if (l == 0) flag_error(P.err, kErrBitPageOOB);
+                continue;
+            }
+            const int64_t prow = (static_cast<int64_t>(pid) * P.Hkv + head) * kPageSize + slot;
+            if constexpr (KB == 16) {
+                dst = (kind == 2 ? P.v_pages : P.k_pages) + prow * kHeadDim;
+            } else {
+                constexpr int kCodeRow = kHeadDim * KB / 8;
+                store_codes<KB>(y, l, off_a, off_b, mask, (kind == 2 ? P.v_codes : P.k_codes) + prow * kCodeRow,
+                                (kind == 2 ? P.v_scales : P.k_scales) + prow);
+                continue;
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + off_a) = a;
+        *reinterpret_cast<uint4 *>(dst + off_b) = b;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <bool kInterleaved>
@@ -402,14 +418,13 @@ auto kernel_for(int code_bits) {
 
 cudaError_t launch_rope(RopeParams p, int code_bits, int sms, cudaStream_t stream) {
     // Warps a token: what takes the fewest rounds of the resident warps, a
-    // round lasting its groups and about two groups' time of start.
-    const int slots = sms * 8 * kWarps;
-    const int keys = code_bits == 0 ? kGroup : kGroup / 2;
-    const int groups = ((p.Hq + 1) / 2 + kGroup - 1) / kGroup + ((p.Hkv + 1) / 2 + keys - 1) / keys;
+    // round lasting its steps and about three steps' time of start.
+    const int slots = sms * kResident * kWarps;
+    const int steps = (p.Hq + 3) / 4 + (code_bits == 0 ? 1 : 2) * ((p.Hkv + 3) / 4);
     int64_t best = INT64_MAX;
-    for (int log2 = 0; log2 <= 3; ++log2) {
+    for (int log2 = 0; log2 <= 4; ++log2) {
         const int64_t warps = static_cast<int64_t>(p.total_q) << log2;
-        const int64_t cost = (warps + slots - 1) / slots * (2 + (groups + (1 << log2) - 1) / (1 << log2));
+        const int64_t cost = (warps + slots - 1) / slots * (3 + (steps + (1 << log2) - 1) / (1 << log2));
         if (cost < best) {
             best = cost;
             p.parts_log2 = log2;
