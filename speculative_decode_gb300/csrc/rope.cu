@@ -274,11 +274,14 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         if (P.positions != nullptr) pos = P.positions[token];
     }
 
-    // where the lane's values stand in a row: its pairs' first and second values
-    // (half a rotation apart), or sixteen in a row
-    const bool rot = l < P.half / 8;
-    const int off_a = kInterleaved || !rot ? 16 * l : 8 * l;
-    const int off_b = kInterleaved || !rot ? off_a + 8 : P.half + 8 * l;
+    // Where the lane's values stand in a row, eight lanes next to one another:
+    // neighbouring pairs in both halves of the row, or its pairs' first and
+    // second values (half a rotation apart), or, behind the rotated ones, both.
+    const int turning = P.half / 8, behind = l - turning;  // lanes with pairs half a rotation apart
+    const bool mine = behind < 0;
+    const int off_a = kInterleaved || mine ? 8 * l : 2 * P.half + 8 * behind;
+    const int off_b = kInterleaved ? 64 + 8 * l : mine ? P.half + 8 * l : off_a + 8 * (8 - turning);
+    const bool rot_a = kInterleaved ? 4 * l < P.half : mine, rot_b = kInterleaved ? 32 + 4 * l < P.half : mine;
     // steps of four rows: the queries', the keys', the values'
     const int nq = (P.Hq + 3) / 4, nk = (P.Hkv + 3) / 4;
     const int steps = nq + (KB == 0 ? nk : 2 * nk);
@@ -315,11 +318,13 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         for (int h = 0; h < 2; ++h) {
             const int j = lane + 32 * h, n = j >> 3, e = j & 7;
             const bool turns = j < P.half;
-            const int pa = kInterleaved ? 2 * j : turns ? j : 16 * n + e;
-            const int pb = kInterleaved ? pa + 1 : turns ? j + P.half : pa + 8;
+            const int pass = 2 * P.half + 8 * (n - turning) + e;
+            const int pa = kInterleaved ? 2 * j : turns ? j : pass;
+            const int pb = kInterleaved ? pa + 1 : turns ? j + P.half : pass + 8 * (8 - turning);
             const float wa = weight != nullptr ? weight[pa] : 1.f, wb = weight != nullptr ? weight[pb] : 1.f;
             const float c = turns ? s_cos[warp][j] : 1.f, s = turns ? s_sin[warp][j] : 0.f;
-            const int at = (e >> 2) * 32 + n * 4 + (e & 3);
+            // neighbouring pairs j: pair (j & 3) + 4 h of lane (j & 31) / 4
+            const int at = kInterleaved ? j : (e >> 2) * 32 + n * 4 + (e & 3);
             s_mul[warp][0][at] = wa * c;
             s_mul[warp][1][at] = -wb * s;
             s_mul[warp][2][at] = wa * s;
@@ -349,20 +354,15 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
             unpack(a, b, kInterleaved, x);
             const float r = weight != nullptr ? norm_factor(x, P.eps, mask) : 1.f;
             const uint64_t rr = two(r, r);
-            if (rot) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const uint64_t A = fma2(x.A[p], product(0, p), mul2(x.B[p], product(1, p)));
-                    const uint64_t B = fma2(x.A[p], product(2, p), mul2(x.B[p], product(3, p)));
-                    x.A[p] = mul2(A, rr);
-                    x.B[p] = mul2(B, rr);
+            for (int p = 0; p < 4; ++p) {
+                uint64_t A = mul2(x.A[p], product(0, p)), B = mul2(x.B[p], product(3, p));
+                if (p < 2 ? rot_a : rot_b) {
+                    A = fma2(x.B[p], product(1, p), A);
+                    B = fma2(x.A[p], product(2, p), B);
                 }
-            } else {
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    x.A[p] = mul2(mul2(x.A[p], product(0, p)), rr);
-                    x.B[p] = mul2(mul2(x.B[p], product(3, p)), rr);
-                }
+                x.A[p] = mul2(A, rr);
+                x.B[p] = mul2(B, rr);
             }
             in_order(x, kInterleaved, y);
             if (KB == 0 || KB == 16 || kind == 0) {
