@@ -420,7 +420,8 @@ SA_API int sa_defrag_apply_bytes(int32_t num_pages, int64_t page_bytes, void *po
  *   y[j], y[j + R/2]       (interleaved 0)
  *   y[2j], y[2j + 1]       (interleaved non-zero)
  * becomes (a cos t - b sin t, a sin t + b cos t); y[R ..] stay. Held in fp32
- * throughout (t in 64 bits, for any int32 position) and rounded once. */
+ * throughout and rounded once; t is reduced exactly, for any int32 position and
+ * any |inv_freq[j]| below 2^24 (others give NaN). */
 typedef struct {
     const float *inv_freq; /* device fp32 [rotary_dim / 2] */
     const float *q_weight; /* device fp32 [128], 16-byte aligned, or NULL: queries have no norm */

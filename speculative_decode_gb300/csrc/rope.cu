@@ -7,8 +7,11 @@
 // (y[2j], y[2j+1]), and (a, b) becomes (a cos t - b sin t, a sin t + b cos t)
 // with t = position * inv_freq[j]. Everything is held in 32 bits and rounded
 // once at the end (bf16 rows) or quantised from the 32-bit values (int8 and
-// int4 page rows). t is formed in 64 bits, as a fraction of a turn: at
-// position 10^6 a 32-bit product would be off by up to 0.06 rad.
+// int4 page rows). t is formed in integers, as a 64-bit fraction of a turn
+// (inv_freq / 2 pi to 64 binary places times the position, whole turns falling
+// off the top, after Payne and Hanek, "Radian reduction for trigonometric
+// functions", 1983): at position 10^6 a 32-bit product would be off by up to
+// 0.06 rad, and 64-bit floating point is slow on this GPU.
 //
 // Eight lanes hold a row, a lane sixteen of its values: eight first and eight
 // second values of pairs where it is rotated, so a rotation stays in the lane.
@@ -68,6 +71,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN where one is
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // A lane's values of a row: A holds the first values of its eight pairs (two in
 // each), B the second.
 struct Values {
@@ -88,18 +102,25 @@ __device__ __forceinline__ void unpack(const uint4 &a, const uint4 &b, bool inte
     }
 }
 
-// The values as they stand in memory: eight at the lane's first place, eight at
-// its second.
-__device__ __forceinline__ void in_order(const Values &v, bool interleaved, float (&y)[16]) {
+// The values as they stand in memory, in pairs: eight at the lane's first place,
+// eight at its second.
+__device__ __forceinline__ void in_order(const Values &v, bool interleaved, uint64_t (&z)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 a = apart(v.A[i]), b = apart(v.B[i]);
         if (interleaved) {
-            y[4 * i] = a.x, y[4 * i + 1] = b.x, y[4 * i + 2] = a.y, y[4 * i + 3] = b.y;
+            const float2 a = apart(v.A[i]), b = apart(v.B[i]);
+            z[2 * i] = two(a.x, b.x);
+            z[2 * i + 1] = two(a.y, b.y);
         } else {
-            y[2 * i] = a.x, y[2 * i + 1] = a.y, y[8 + 2 * i] = b.x, y[8 + 2 * i + 1] = b.y;
+            z[i] = v.A[i];
+            z[4 + i] = v.B[i];
         }
     }
+}
+
+__device__ __forceinline__ uint32_t pack(uint64_t v) {
+    const float2 p = apart(v);
+    return pack_bf16x2(p.x, p.y);
 }
 
 // The factor rsqrt(mean(x^2) + eps) of a row. A sum of squares past 32 bits is
@@ -136,49 +157,90 @@ __device__ __forceinline__ float norm_factor(Values &v, float eps, uint32_t mask
     return r;
 }
 
+// freq / (2 pi) modulo 1 in units of 2^-64: the 24 bits of freq times 1 / (2 pi) to
+// 128 binary places, shifted by its exponent. |freq| is below 2^24.
+__device__ __forceinline__ uint64_t turn_of(float freq) {
+    const uint32_t bits = __float_as_uint(freq);
+    const int exponent = static_cast<int>(bits >> 23 & 255);
+    const uint64_t m = exponent != 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;
+    const uint64_t p0 = m * 0x7d4d3770u;
+    const uint64_t p1 = m * 0x7f09d5f4u + (p0 >> 32);
+    const uint64_t p2 = m * 0x9391054au + (p1 >> 32);
+    const uint64_t p3 = m * 0x28be60dbu + (p2 >> 32);
+    const uint64_t low = p3 << 32 | (p2 & 0xffffffffu), high = p3 >> 32;
+    const int shift = 150 - exponent;
+    const uint64_t turn = shift <= 0   ? low
+                          : shift < 64 ? low >> shift | high << (64 - shift)
+                          : shift < 96 ? high >> (shift - 64)
+                                       : 0;
+    return bits >> 31 ? 0 - turn : turn;
+}
+
+// cos and sin of pos turns of that size.
+__device__ __forceinline__ void cos_sin(uint64_t turn, int pos, bool known, float *c, float *s) {
+    const uint64_t at = turn * static_cast<uint64_t>(static_cast<int64_t>(pos));
+    // in half turns from -1 to 1
+    const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f;
+    sincospif(known ? half_turns : NAN, s, c);
+}
+
 // The page format of the quantising appends (see kv_append.cu): scale = amax /
 // Cmax and code = round-half-even(y / scale), both by IEEE division. The
-// quotient is taken as a product first, which is off by less than 127 * 2^-21;
-// only where that may change the code is it divided. The lane's values stand at
-// a .. a + 7 and b .. b + 7.
+// quotient is taken as a product first, which is off by less than 127 * 2^-21,
+// and rounded by adding 1.5 * 2^23, whose low bits then are the code; where a
+// quotient lies near the border of two codes, the row's are divided. z: the
+// lane's values as they stand in memory, at a .. a + 7 and b .. b + 7.
 template <int KB>
-__device__ __forceinline__ void store_codes(const float (&y)[16], int l, int a, int b, uint32_t mask, uint8_t *codes,
+__device__ __forceinline__ void store_codes(const uint64_t (&z)[8], int l, int a, int b, uint32_t mask, uint8_t *codes,
                                             float *scale) {
-    constexpr int kMax = KB == 8 ? 127 : 7;
+    constexpr int kMax = KB == 8 ? 127 : 7, kOffset = KB == 8 ? 0 : 8;
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(y[e]));
+    for (int i = 0; i < 8; ++i) {
+        const float2 p = apart(z[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(p.x), fabsf(p.y)));
+    }
     amax = row_max(amax, mask);
     const float sc = __fdiv_rn(amax, static_cast<float>(kMax));
-    const bool plain = sc > 1e-30f;
-    const float inv = plain ? __frcp_rn(sc) : 0.f;
-    int c[16];
-    uint32_t unsure = plain ? 0u : 0xffffu;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sc));
+    const float whole = 12582912.f + kOffset;
+    const uint64_t inv2 = two(inv, inv), up = two(whole, whole), down = two(-whole, -whole), minus = two(-1.f, -1.f);
+    uint32_t c[16];
+    float border = 1.f;  // distance of a quotient from the nearest border
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float q = y[e] * inv;
-        c[e] = __float2int_rn(q);
-        const float off = fabsf(q - static_cast<float>(c[e]));
-        unsure |= static_cast<uint32_t>(fabsf(off - 0.5f) < 1e-3f) << e;
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t q = mul2(z[i], inv2);
+        const uint64_t r = add2(q, up);
+        const float2 off = apart(fma2(add2(r, down), minus, q)), bits = apart(r);
+        border = min_nan(border, fabsf(fabsf(off.x) - 0.5f));
+        border = min_nan(border, fabsf(fabsf(off.y) - 0.5f));
+        c[2 * i] = __float_as_uint(bits.x);
+        c[2 * i + 1] = __float_as_uint(bits.y);
     }
-    if (unsure != 0) {
+    if (!(border >= 1e-3f && sc > 1e-30f)) {  // NaN among them
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (unsure >> e & 1) c[e] = sc > 0.f ? __float2int_rn(__fdiv_rn(y[e], sc)) : 0;
-    }
-    uint32_t packed[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const int k = max(-kMax, min(kMax, c[e]));
-        if constexpr (KB == 8) packed[e / 4] |= (static_cast<uint32_t>(k) & 0xffu) << (8 * (e & 3));
-        else packed[e / 8] |= static_cast<uint32_t>(k + 8) << (4 * (e & 7));
+        for (int i = 0; i < 8; ++i) {
+            const float2 p = apart(z[i]);
+            const int x = sc > 0.f ? __float2int_rn(__fdiv_rn(p.x, sc)) : 0, y = sc > 0.f ? __float2int_rn(__fdiv_rn(p.y, sc)) : 0;
+            c[2 * i] = static_cast<uint32_t>(max(-kMax, min(kMax, x)) + kOffset);
+            c[2 * i + 1] = static_cast<uint32_t>(max(-kMax, min(kMax, y)) + kOffset);
+        }
     }
     if constexpr (KB == 8) {
-        *reinterpret_cast<uint2 *>(codes + a) = make_uint2(packed[0], packed[1]);
-        *reinterpret_cast<uint2 *>(codes + b) = make_uint2(packed[2], packed[3]);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+                               0x5410);
+        *reinterpret_cast<uint2 *>(codes + a) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(codes + b) = make_uint2(w[2], w[3]);
     } else {
-        *reinterpret_cast<uint32_t *>(codes + a / 2) = packed[0];
-        *reinterpret_cast<uint32_t *>(codes + b / 2) = packed[1];
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 15; e >= 0; --e) w[e / 8] = w[e / 8] << 4 | (c[e] & 15u);
+        *reinterpret_cast<uint32_t *>(codes + a / 2) = w[0];
+        *reinterpret_cast<uint32_t *>(codes + b / 2) = w[1];
     }
     if (l == 0) *scale = sc;
 }
@@ -254,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     // two angles a lane
     const float freq0 = lane < P.half ? P.inv_freq[lane] : 0.f;
     const float freq1 = lane + 32 < P.half ? P.inv_freq[lane + 32] : 0.f;
+    const uint64_t turn0 = turn_of(freq0), turn1 = turn_of(freq1);
 
     int pos, pid = 0, slot = 0;
     if constexpr (KB == 0) {
@@ -304,12 +367,8 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     for (int a = 0; a < kAhead; ++a) fetch(part + a * parts, a);
 
     // the token's angles, while the first rows are on their way
-    auto angle = [&](float freq, int j) {
-        const double turns = static_cast<double>(pos) * (static_cast<double>(freq) * 0.15915494309189535);
-        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s_sin[warp][j], &s_cos[warp][j]);
-    };
-    if (lane < P.half) angle(freq0, lane);
-    if (lane + 32 < P.half) angle(freq1, lane + 32);
+    if (lane < P.half) cos_sin(turn0, pos, fabsf(freq0) < 0x1p24f, &s_cos[warp][lane], &s_sin[warp][lane]);
+    if (lane + 32 < P.half) cos_sin(turn1, pos, fabsf(freq1) < 0x1p24f, &s_cos[warp][lane + 32], &s_sin[warp][lane + 32]);
     __syncwarp();
     // a kind's products: pair e of lane n's values, two pairs a lane
     auto prepare = [&](const float *weight) {
@@ -348,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         fetch(i + kAhead * parts, at);
         at = at + 1 == kAhead ? 0 : at + 1;
         const bool here = head < (kind == 0 ? P.Hq : P.Hkv);  // all the row's lanes
-        float y[16];
+        uint64_t z[8];
         if (kind != 2) {
             Values x;
             unpack(a, b, kInterleaved, x);
@@ -364,20 +423,15 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
                 x.A[p] = mul2(A, rr);
                 x.B[p] = mul2(B, rr);
             }
-            in_order(x, kInterleaved, y);
+            in_order(x, kInterleaved, z);
             if (KB == 0 || KB == 16 || kind == 0) {
-                a = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                               pack_bf16x2(y[6], y[7]));
-                b = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
-                               pack_bf16x2(y[14], y[15]));
+                a = make_uint4(pack(z[0]), pack(z[1]), pack(z[2]), pack(z[3]));
+                b = make_uint4(pack(z[4]), pack(z[5]), pack(z[6]), pack(z[7]));
             }
         } else if constexpr (KB == 8 || KB == 4) {
             const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[2 * e] = bf16_lo(w[e]);
-                y[2 * e + 1] = bf16_hi(w[e]);
-            }
+            for (int e = 0; e < 8; ++e) z[e] = two(bf16_lo(w[e]), bf16_hi(w[e]));
         }
         if (!here) continue;
         uint16_t *dst = nullptr;
@@ -395,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
                 dst = (kind == 2 ? P.v_pages : P.k_pages) + prow * kHeadDim;
             } else {
                 constexpr int kCodeRow = kHeadDim * KB / 8;
-                store_codes<KB>(y, l, off_a, off_b, mask, (kind == 2 ? P.v_codes : P.k_codes) + prow * kCodeRow,
+                store_codes<KB>(z, l, off_a, off_b, mask, (kind == 2 ? P.v_codes : P.k_codes) + prow * kCodeRow,
                                 (kind == 2 ? P.v_scales : P.k_scales) + prow);
                 continue;
             }
