@@ -356,6 +356,7 @@ class _Types:
         import torch
         self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)  # values or bit patterns
         self.f32 = (torch.float32,)
+        self.int32 = torch.int32
         self.i32 = (torch.int32,)
         self.i8 = (torch.int8,)
         self.u8 = (torch.uint8,)
@@ -387,9 +388,17 @@ def _refuse(t, name: str, dtypes, here: int, shape=None) -> None:
 
 def _tensor(t, name: str, dtypes, here: int, shape=None) -> int:
     """Address of a packed tensor of one of these dtypes (and of that shape) on the current device."""
-    if (t is None or t.get_device() != here or t.dtype not in dtypes or not t.is_contiguous() or
+    if (t is None or t.dtype not in dtypes or t.get_device() != here or not t.is_contiguous() or
             (shape is not None and t.shape != shape)):
         _refuse(t, name, dtypes, here, shape)
+    return t.data_ptr()
+
+
+def _ints(t, name: str, here: int, count: int) -> int:
+    """Address of packed int32 values, `count` of them (the attributes that cost a call least)."""
+    if t is None or t.dtype is not _types_made.int32 or t.get_device() != here or t.numel() != count or \
+            not t.is_contiguous():
+        _refuse(t, name, _types_made.i32, here, (count,))
     return t.data_ptr()
 
 
@@ -453,7 +462,7 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
         hk = k.shape[1]
         kp, ks = _heads(k, "k", n, hk, here)
         ko, kos = _heads(k_out, "k_out", n, hk, here)
-    pos = _tensor(positions, "positions", _types_made.i32, here, (n,))
+    pos = _ints(positions, "positions", here, n)
     rc = load_library().sa_qk_norm_rope(rope._on(here), n, hq, hk, 128, qp, qs, kp, ks, pos, qo, qos, ko, kos,
                                         _stream(stream))
     if rc:
@@ -462,7 +471,7 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
 
 def _append_rope(name, dims, rope, q, k_new, v_new, q_out, pools, pool_types, block_table, seq_lens, q_lens,
                  positions, err_flag, stream) -> None:
-    here, i32 = _here(), _types_made.i32
+    here = _here()
     n, hkv, pages, B = dims.total_q, dims.num_kv_heads, dims.num_pages, dims.num_seqs
     qp, qs, qo = None, 0, None
     if q is not None or q_out is not None:
@@ -473,11 +482,11 @@ def _append_rope(name, dims, rope, q, k_new, v_new, q_out, pools, pool_types, bl
     vp, vs = _heads(v_new, "v_new", n, hkv, here)
     addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
                  for t, (dt, row) in zip(pools, pool_types)]
-    bt = _tensor(block_table, "block_table", i32, here, (B, dims.max_pages_per_seq))
-    sl = _tensor(seq_lens, "seq_lens", i32, here, (B,))
-    ql = _tensor(q_lens, "q_lens", i32, here, (B,))
-    ps = None if positions is None else _tensor(positions, "positions", i32, here, (n,))
-    err = None if err_flag is None else _tensor(err_flag, "err_flag", i32, here)
+    bt = _tensor(block_table, "block_table", _types_made.i32, here, (B, dims.max_pages_per_seq))
+    sl = _ints(seq_lens, "seq_lens", here, B)
+    ql = _ints(q_lens, "q_lens", here, B)
+    ps = None if positions is None else _ints(positions, "positions", here, n)
+    err = None if err_flag is None else _ints(err_flag, "err_flag", here, 1)
     rc = getattr(load_library(), name)(ctypes.byref(dims), rope._on(here), qp, qs, kp, ks, vp, vs, qo, *addresses, bt, sl,
                                        ql, ps, err, _stream(stream))
     if rc:
@@ -536,13 +545,13 @@ def beam_select(logits, scores, tokens, parents, scores_out, workspace, finished
     if B * W <= 1:
         row = V
     K = tokens.shape[-1]
-    picks, beams, i32, f32 = (B, K), (B, W), types.i32, types.f32
+    picks, beams, f32 = (B, K), (B, W), types.f32
     sc = _tensor(scores, "scores", f32, here, beams)
-    fi = None if finished is None else _tensor(finished, "finished", i32, here, beams)
-    to = _tensor(tokens, "tokens", i32, here, picks)
-    pa = _tensor(parents, "parents", i32, here, picks)
+    fi = None if finished is None else _ints(finished, "finished", here, B * W)
+    to = _tensor(tokens, "tokens", types.i32, here, picks)
+    pa = _tensor(parents, "parents", types.i32, here, picks)
     so = _tensor(scores_out, "scores_out", f32, here, picks)
-    fo = None if finished_out is None else _tensor(finished_out, "finished_out", i32, here, picks)
+    fo = None if finished_out is None else _ints(finished_out, "finished_out", here, B * K)
     ws = _tensor(workspace, "workspace", types.u8, here)
     lib = load_library()
     rc = (lib.sa_beam_select if wide else lib.sa_beam_select_bf16)(
@@ -558,13 +567,11 @@ def _beam_reorder(name, dims, beam_width, parents, block_table, seq_lens, block_
     table = (B, dims.max_pages_per_seq)
     addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
                  for t, (dt, row) in zip(pools, pool_types)]
-    pa = _tensor(parents, "parents", i32, here)
-    if parents.numel() != B:
-        raise ValueError(f"parents: {parents.numel()} values for {B} sequences")
+    pa = _ints(parents, "parents", here, B)
     bt = _tensor(block_table, "block_table", i32, here, table)
-    sl = _tensor(seq_lens, "seq_lens", i32, here, (B,))
+    sl = _ints(seq_lens, "seq_lens", here, B)
     bo = _tensor(block_table_out, "block_table_out", i32, here, table)
-    err = None if err_flag is None else _tensor(err_flag, "err_flag", i32, here)
+    err = None if err_flag is None else _ints(err_flag, "err_flag", here, 1)
     rc = getattr(load_library(), name)(ctypes.byref(dims), beam_width, pa, bt, sl, bo, *addresses, err, _stream(stream))
     if rc:
         _check(rc, name)

@@ -20,7 +20,7 @@
 // kept in shared memory. A warp turns four rows at a time, in packed 32-bit
 // arithmetic, about a hundred instructions. It takes one token, or every
 // `parts`-th four rows of one; the loads go through a ring in shared memory
-// (asynchronous copies, each lane its own bytes, so no barrier), four steps
+// (asynchronous copies, each lane its own bytes, so no barrier), three steps
 // ahead. Bound: bytes moved (a row in, a row out) for many tokens, two
 // dependent memory round trips (lengths, then rows) for few.
 #include <cfloat>
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;    // steps of four rows in flight per warp
+constexpr int kAhead = 3;    // steps of four rows in flight per warp
 constexpr int kResident = 8; // CTAs per SM
 
 // Sum and maximum over a row's eight lanes.
@@ -162,17 +162,17 @@ __device__ __forceinline__ float norm_factor(Values &v, float eps, uint32_t mask
 __device__ __forceinline__ uint64_t turn_of(float freq) {
     const uint32_t bits = __float_as_uint(freq);
     const int exponent = static_cast<int>(bits >> 23 & 255);
-    const uint64_t m = exponent != 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;
-    const uint64_t p0 = m * 0x7d4d3770u;
-    const uint64_t p1 = m * 0x7f09d5f4u + (p0 >> 32);
-    const uint64_t p2 = m * 0x9391054au + (p1 >> 32);
-    const uint64_t p3 = m * 0x28be60dbu + (p2 >> 32);
-    const uint64_t low = p3 << 32 | (p2 & 0xffffffffu), high = p3 >> 32;
-    const int shift = 150 - exponent;
-    const uint64_t turn = shift <= 0   ? low
-                          : shift < 64 ? low >> shift | high << (64 - shift)
-                          : shift < 96 ? high >> (shift - 64)
-                                       : 0;
+    const uint32_t m = exponent != 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;
+    auto times = [m](uint32_t part, uint64_t carry) { return static_cast<uint64_t>(m) * part + (carry >> 32); };
+    const uint64_t p0 = times(0x7d4d3770u, 0), p1 = times(0x7f09d5f4u, p0), p2 = times(0x9391054au, p1),
+                   p3 = times(0x28be60dbu, p2);
+    // bits 64 .. 159 of the product in three words, shifted right word by word
+    uint32_t w0 = static_cast<uint32_t>(p2), w1 = static_cast<uint32_t>(p3), w2 = static_cast<uint32_t>(p3 >> 32);
+    int shift = max(0, 150 - exponent);
+    if (shift >= 32) w0 = w1, w1 = w2, w2 = 0, shift -= 32;
+    if (shift >= 32) w0 = w1, w1 = 0, shift -= 32;
+    if (shift >= 32) w0 = 0, shift = 0;
+    const uint64_t turn = static_cast<uint64_t>(__funnelshift_r(w1, w2, shift)) << 32 | __funnelshift_r(w0, w1, shift);
     return bits >> 31 ? 0 - turn : turn;
 }
 
@@ -186,14 +186,15 @@ __device__ __forceinline__ void cos_sin(uint64_t turn, int pos, bool known, floa
 
 // The page format of the quantising appends (see kv_append.cu): scale = amax /
 // Cmax and code = round-half-even(y / scale), both by IEEE division. The
-// quotient is taken as a product first, which is off by less than 127 * 2^-21,
-// and rounded by adding 1.5 * 2^23, whose low bits then are the code; where a
-// quotient lies near the border of two codes, the row's are divided. z: the
-// lane's values as they stand in memory, at a .. a + 7 and b .. b + 7.
+// quotient is taken as a product with the reciprocal first, and rounded by
+// adding 1.5 * 2^23, whose low bits then are the code; where a quotient lies near
+// the border of two codes, the row's are divided. z: the lane's values as they
+// stand in memory, at a .. a + 7 and b .. b + 7.
 template <int KB>
 __device__ __forceinline__ void store_codes(const uint64_t (&z)[8], int l, int a, int b, uint32_t mask, uint8_t *codes,
                                             float *scale) {
     constexpr int kMax = KB == 8 ? 127 : 7, kOffset = KB == 8 ? 0 : 8;
+    constexpr float kBorder = KB == 8 ? 0x1p-15f : 0x1p-19f;  // above kMax (2^-23 + 2^-24), the product's error
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -218,7 +219,7 @@ __device__ __forceinline__ void store_codes(const uint64_t (&z)[8], int l, int a
         c[2 * i] = __float_as_uint(bits.x);
         c[2 * i + 1] = __float_as_uint(bits.y);
     }
-    if (!(border >= 1e-3f && sc > 1e-30f)) {  // NaN among them
+    if (!(border >= kBorder && sc > 1e-30f)) {  // NaN among them
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 p = apart(z[i]);
@@ -256,41 +257,46 @@ struct TokenPlace {
 // seq is -1 behind the last row. Block 0 also checks every sequence (each block
 // skips the rows of a bad one).
 __device__ __forceinline__ void locate(const RopeParams &P, int token, TokenPlace (&place)[kWarps]) {
-    __shared__ long long s_total[kWarps];
+    __shared__ uint32_t s_total[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // rows are counted up to one past the last
+    const uint32_t cap = static_cast<uint32_t>(P.total_q) + 1;
+    auto plus = [cap](uint32_t a, uint32_t b) { return min(a + b, cap); };
+    auto rows_of = [&](int n) { return min(static_cast<uint32_t>(max(n, 0)), cap); };
     const int per = (P.B + kThreads - 1) / kThreads;
     const int lo = min(P.B, static_cast<int>(threadIdx.x) * per), hi = min(P.B, lo + per);
-    long long sum = 0;
-    for (int b = lo; b < hi; ++b) sum += max(P.q_lens[b], 0);
-    const int len0 = lo < hi ? P.seq_lens[lo] : 0;
-    long long incl = sum;
+    const int n0 = lo < hi ? P.q_lens[lo] : 0, len0 = lo < hi ? P.seq_lens[lo] : 0;
+    uint32_t sum = rows_of(n0);
+    for (int b = lo + 1; b < hi; ++b) sum = plus(sum, rows_of(P.q_lens[b]));
+    uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl = plus(incl, up);
     }
+    uint32_t at = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) at = 0;
     if (lane == 31) s_total[warp] = incl;
     if (threadIdx.x < kWarps) place[threadIdx.x].seq = -1;
     __syncthreads();
-    long long at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += s_total[w];
+    for (int w = 0; w < warp; ++w) at = plus(at, s_total[w]);
     if (blockIdx.x == 0) {
         bool bad = false;
-        long long a = at;
+        uint32_t a = at;
         for (int b = lo; b < hi; ++b) {
             const int n = P.q_lens[b];
-            a += max(n, 0);
-            bad |= n < 0 || n > P.seq_lens[b] || n > P.max_q_len || a > P.total_q;
+            a = plus(a, rows_of(n));
+            bad |= n < 0 || n > P.seq_lens[b] || n > P.max_q_len || a == cap;
         }
         if (bad) flag_error(P.err, kErrBitQlen);
     }
-    if (at < token + kWarps && at + sum > token) {
-        for (int b = lo; b < hi && at < token + kWarps; ++b) {
-            const int n = max(P.q_lens[b], 0);
-            for (int k = 0; k < kWarps; ++k)
-                if (token + k >= at && token + k < at + n)
-                    place[k] = TokenPlace{b, n, b == lo ? len0 : P.seq_lens[b], static_cast<int>(at)};
-            at += n;
+    const uint32_t first = token, end = first + kWarps;
+    if (at < end && plus(at, sum) > first) {
+        for (int b = lo; b < hi && at < end; ++b) {
+            const uint32_t n = rows_of(b == lo ? n0 : P.q_lens[b]), next = plus(at, n);
+            for (uint32_t row = max(at, first); row < min(next, end); ++row)
+                place[row - first] = TokenPlace{b, static_cast<int>(n), b == lo ? len0 : P.seq_lens[b], static_cast<int>(at)};
+            at = next;
         }
     }
     __syncthreads();
@@ -316,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     // two angles a lane
     const float freq0 = lane < P.half ? P.inv_freq[lane] : 0.f;
     const float freq1 = lane + 32 < P.half ? P.inv_freq[lane + 32] : 0.f;
-    const uint64_t turn0 = turn_of(freq0), turn1 = turn_of(freq1);
 
     int pos, pid = 0, slot = 0;
     if constexpr (KB == 0) {
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     for (int a = 0; a < kAhead; ++a) fetch(part + a * parts, a);
 
     // the token's angles, while the first rows are on their way
+    const uint64_t turn0 = turn_of(freq0), turn1 = turn_of(freq1);
     if (lane < P.half) cos_sin(turn0, pos, fabsf(freq0) < 0x1p24f, &s_cos[warp][lane], &s_sin[warp][lane]);
     if (lane + 32 < P.half) cos_sin(turn1, pos, fabsf(freq1) < 0x1p24f, &s_cos[warp][lane + 32], &s_sin[warp][lane + 32]);
     __syncwarp();
