@@ -469,28 +469,38 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
         _check(rc, "sa_qk_norm_rope")
 
 
-def _append_rope(name, dims, rope, q, k_new, v_new, q_out, pools, pool_types, block_table, seq_lens, q_lens,
-                 positions, err_flag, stream) -> None:
-    here = _here()
-    n, hkv, pages, B = dims.total_q, dims.num_kv_heads, dims.num_pages, dims.num_seqs
-    qp, qs, qo = None, 0, None
-    if q is not None or q_out is not None:
+def _pools(dims: Dims, here: int, k_pages, v_pages):
+    """Addresses of bf16 page pools."""
+    bf16, shape = _types_made.bf16, (dims.num_pages, dims.num_kv_heads, 256, 128)
+    return _tensor(k_pages, "k_pages", bf16, here, shape), _tensor(v_pages, "v_pages", bf16, here, shape)
+
+
+def _code_pools(dims: Dims, here: int, dtypes, row: int, k_codes, v_codes, k_scales, v_scales):
+    """Addresses of code pools (rows of `row` bytes) and their scales."""
+    f32, rows = _types_made.f32, (dims.num_pages, dims.num_kv_heads, 256)
+    codes = (*rows, row)
+    return (_tensor(k_codes, "k_codes", dtypes, here, codes), _tensor(v_codes, "v_codes", dtypes, here, codes),
+            _tensor(k_scales, "k_scales", f32, here, rows), _tensor(v_scales, "v_scales", f32, here, rows))
+
+
+def _append_rope(call, what, here, dims, rope, q, k_new, v_new, q_out, pools, block_table, seq_lens, q_lens, positions,
+                 err_flag, stream) -> None:
+    n, hkv, B = dims.total_q, dims.num_kv_heads, dims.num_seqs
+    if q is None and q_out is None:
+        qp, qs, qo = None, 0, None
+    else:
         hq = dims.num_q_heads
         qp, qs = _heads(q, "q", n, hq, here)
         qo = _tensor(q_out, "q_out", _types_made.bf16, here, (n, hq, 128))
     kp, ks = _heads(k_new, "k_new", n, hkv, here)
     vp, vs = _heads(v_new, "v_new", n, hkv, here)
-    addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
-                 for t, (dt, row) in zip(pools, pool_types)]
-    bt = _tensor(block_table, "block_table", _types_made.i32, here, (B, dims.max_pages_per_seq))
-    sl = _ints(seq_lens, "seq_lens", here, B)
-    ql = _ints(q_lens, "q_lens", here, B)
-    ps = None if positions is None else _ints(positions, "positions", here, n)
-    err = None if err_flag is None else _ints(err_flag, "err_flag", here, 1)
-    rc = getattr(load_library(), name)(ctypes.byref(dims), rope._on(here), qp, qs, kp, ks, vp, vs, qo, *addresses, bt, sl,
-                                       ql, ps, err, _stream(stream))
+    rc = call(ctypes.byref(dims), rope._on(here), qp, qs, kp, ks, vp, vs, qo, *pools,
+              _tensor(block_table, "block_table", _types_made.i32, here, (B, dims.max_pages_per_seq)),
+              _ints(seq_lens, "seq_lens", here, B), _ints(q_lens, "q_lens", here, B),
+              None if positions is None else _ints(positions, "positions", here, n),
+              None if err_flag is None else _ints(err_flag, "err_flag", here, 1), _stream(stream))
     if rc:
-        _check(rc, name)
+        _check(rc, what)
 
 
 def kv_append_rope(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, q_lens,
@@ -498,27 +508,27 @@ def kv_append_rope(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_pages, v_pa
     """sa_kv_append_rope: kv_append with the keys normalised and rotated on the
     way, and q -> q_out for paged_attn (q and q_out may be None). q, k_new and
     v_new may be views with any token stride (a multiple of 8 values)."""
-    bf16 = _types().bf16
-    _append_rope("sa_kv_append_rope", dims, rope, q, k_new, v_new, q_out, (k_pages, v_pages), ((bf16, 128),) * 2,
-                 block_table, seq_lens, q_lens, positions, err_flag, stream)
+    here = _here()
+    _append_rope(load_library().sa_kv_append_rope, "sa_kv_append_rope", here, dims, rope, q, k_new, v_new, q_out,
+                 _pools(dims, here, k_pages, v_pages), block_table, seq_lens, q_lens, positions, err_flag, stream)
 
 
 def kv_append_rope_q8(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_codes, v_codes, k_scales, v_scales,
                       block_table, seq_lens, q_lens, positions=None, err_flag=None, stream=None) -> None:
     """kv_append_rope into int8 pages (pools as in kv_append_q8)."""
-    t = _types()
-    _append_rope("sa_kv_append_rope_q8", dims, rope, q, k_new, v_new, q_out, (k_codes, v_codes, k_scales, v_scales),
-                 ((t.i8, 128), (t.i8, 128), (t.f32, 0), (t.f32, 0)), block_table, seq_lens, q_lens, positions, err_flag,
-                 stream)
+    here = _here()
+    _append_rope(load_library().sa_kv_append_rope_q8, "sa_kv_append_rope_q8", here, dims, rope, q, k_new, v_new, q_out,
+                 _code_pools(dims, here, _types_made.i8, 128, k_codes, v_codes, k_scales, v_scales), block_table, seq_lens,
+                 q_lens, positions, err_flag, stream)
 
 
 def kv_append_rope_q4(dims: Dims, rope: Rope, q, k_new, v_new, q_out, k_codes, v_codes, k_scales, v_scales,
                       block_table, seq_lens, q_lens, positions=None, err_flag=None, stream=None) -> None:
     """kv_append_rope into int4 pages (pools as in kv_append_q4)."""
-    t = _types()
-    _append_rope("sa_kv_append_rope_q4", dims, rope, q, k_new, v_new, q_out, (k_codes, v_codes, k_scales, v_scales),
-                 ((t.u8, 64), (t.u8, 64), (t.f32, 0), (t.f32, 0)), block_table, seq_lens, q_lens, positions, err_flag,
-                 stream)
+    here = _here()
+    _append_rope(load_library().sa_kv_append_rope_q4, "sa_kv_append_rope_q4", here, dims, rope, q, k_new, v_new, q_out,
+                 _code_pools(dims, here, _types_made.u8, 64, k_codes, v_codes, k_scales, v_scales), block_table, seq_lens,
+                 q_lens, positions, err_flag, stream)
 
 
 def beam_select_workspace_size(num_groups: int, beam_width: int, vocab: int, num_select: int) -> int:
@@ -560,45 +570,40 @@ def beam_select(logits, scores, tokens, parents, scores_out, workspace, finished
         _check(rc, "sa_beam_select" if wide else "sa_beam_select_bf16")
 
 
-def _beam_reorder(name, dims, beam_width, parents, block_table, seq_lens, block_table_out, pools, pool_types, err_flag,
+def _beam_reorder(call, what, here, dims, beam_width, parents, block_table, seq_lens, block_table_out, pools, err_flag,
                   stream) -> None:
-    here, i32 = _here(), _types_made.i32
-    B, hkv, pages = dims.num_seqs, dims.num_kv_heads, dims.num_pages
+    i32, B = _types_made.i32, dims.num_seqs
     table = (B, dims.max_pages_per_seq)
-    addresses = [_tensor(t, "page pool", dt, here, (pages, hkv, 256, row) if row else (pages, hkv, 256))
-                 for t, (dt, row) in zip(pools, pool_types)]
-    pa = _ints(parents, "parents", here, B)
-    bt = _tensor(block_table, "block_table", i32, here, table)
-    sl = _ints(seq_lens, "seq_lens", here, B)
-    bo = _tensor(block_table_out, "block_table_out", i32, here, table)
-    err = None if err_flag is None else _ints(err_flag, "err_flag", here, 1)
-    rc = getattr(load_library(), name)(ctypes.byref(dims), beam_width, pa, bt, sl, bo, *addresses, err, _stream(stream))
+    rc = call(ctypes.byref(dims), beam_width, _ints(parents, "parents", here, B),
+              _tensor(block_table, "block_table", i32, here, table), _ints(seq_lens, "seq_lens", here, B),
+              _tensor(block_table_out, "block_table_out", i32, here, table), *pools,
+              None if err_flag is None else _ints(err_flag, "err_flag", here, 1), _stream(stream))
     if rc:
-        _check(rc, name)
+        _check(rc, what)
 
 
 def beam_reorder(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_pages, v_pages,
                  err_flag=None, stream=None) -> None:
     """sa_beam_reorder: the tables of the chosen continuations, and the copies of
     the tail pages that more than one of them continues."""
-    bf16 = _types().bf16
-    _beam_reorder("sa_beam_reorder", dims, beam_width, parents, block_table, seq_lens, block_table_out,
-                  (k_pages, v_pages), ((bf16, 128),) * 2, err_flag, stream)
+    here = _here()
+    _beam_reorder(load_library().sa_beam_reorder, "sa_beam_reorder", here, dims, beam_width, parents, block_table, seq_lens,
+                  block_table_out, _pools(dims, here, k_pages, v_pages), err_flag, stream)
 
 
 def beam_reorder_q8(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_codes, v_codes,
                     k_scales, v_scales, err_flag=None, stream=None) -> None:
     """beam_reorder over int8 pages."""
-    t = _types()
-    _beam_reorder("sa_beam_reorder_q8", dims, beam_width, parents, block_table, seq_lens, block_table_out,
-                  (k_codes, v_codes, k_scales, v_scales), ((t.i8, 128), (t.i8, 128), (t.f32, 0), (t.f32, 0)), err_flag,
-                  stream)
+    here = _here()
+    _beam_reorder(load_library().sa_beam_reorder_q8, "sa_beam_reorder_q8", here, dims, beam_width, parents, block_table,
+                  seq_lens, block_table_out,
+                  _code_pools(dims, here, _types_made.i8, 128, k_codes, v_codes, k_scales, v_scales), err_flag, stream)
 
 
 def beam_reorder_q4(dims: Dims, beam_width: int, parents, block_table, seq_lens, block_table_out, k_codes, v_codes,
                     k_scales, v_scales, err_flag=None, stream=None) -> None:
     """beam_reorder over int4 pages."""
-    t = _types()
-    _beam_reorder("sa_beam_reorder_q4", dims, beam_width, parents, block_table, seq_lens, block_table_out,
-                  (k_codes, v_codes, k_scales, v_scales), ((t.u8, 64), (t.u8, 64), (t.f32, 0), (t.f32, 0)), err_flag,
-                  stream)
+    here = _here()
+    _beam_reorder(load_library().sa_beam_reorder_q4, "sa_beam_reorder_q4", here, dims, beam_width, parents, block_table,
+                  seq_lens, block_table_out,
+                  _code_pools(dims, here, _types_made.u8, 64, k_codes, v_codes, k_scales, v_scales), err_flag, stream)

@@ -213,6 +213,6 @@ def test_binding_refuses_host_tensors(sa):
                        z(1 << 20, dtype=torch.uint8))
     d = sa.dims_for(2, 8, 2, 4, 2, 2, 1)
     pool = z(4, 2, 256, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="page pool"):
+    with pytest.raises(ValueError, match="k_pages"):
         sa.beam_reorder(d, 2, z(2, dtype=torch.int32), z(2, 2, dtype=torch.int32), z(2, dtype=torch.int32),
                         z(2, 2, dtype=torch.int32), pool, pool)
