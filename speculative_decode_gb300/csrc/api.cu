@@ -744,7 +744,8 @@ static int append_rope(const sa_dims *dims, const sa_rope *rope, RopeParams &p, 
     const sa_dims &d = *dims;
     rc = check_rope(rope, d.head_dim);
     if (rc) return rc;
-    if (d.num_q_heads > kMaxRopeHeads) return SA_ERR_UNSUPPORTED;
+    // the kernel counts rows in 32 bits
+    if (d.num_q_heads > kMaxRopeHeads || d.total_q > (1 << 30)) return SA_ERR_UNSUPPORTED;
     if ((p.q == nullptr) != (p.q_out == nullptr)) return SA_ERR_ARG;
     if (d.num_seqs == 0 || d.total_q == 0) return SA_OK;
     const int64_t hq = p.q == nullptr ? 0 : d.num_q_heads;

@@ -405,9 +405,11 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     uint64_t mine[kMine];
 #pragma unroll
     for (int u = 0; u < kMine; ++u) {
+        mine[u] = 0;
+        if (u * kThreads >= lists * R) continue;  // for the whole block
         unsigned w, chunk, rank;
         place(entry_of(u), 0, w, chunk, rank);
-        mine[u] = entry_of(u) < lists * R ? key_of(w, chunk, rank) : 0;
+        if (entry_of(u) < lists * R) mine[u] = key_of(w, chunk, rank);
     }
     if (t < P.W) {
         S.score[t] = P.scores[row0 + t];
@@ -464,10 +466,15 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
             const unsigned e = e0 + entry_of(u);
-            unsigned w, chunk, rank;
-            place(e, rank0, w, chunk, rank);
             most[u] = -INFINITY;
             of[u] = 0;
+            last_rank[u] = false;
+            if (e0 + u * kThreads >= lists * R) {  // for the whole block
+                mine[u] = 0;
+                continue;
+            }
+            unsigned w, chunk, rank;
+            place(e, rank0, w, chunk, rank);
             last_rank[u] = rank == rank0 + R - 1;
             if (e >= lists * R) {
                 mine[u] = 0;

@@ -152,6 +152,7 @@ def test_kv_append_rope_refuses(sa):
         assert call(dims=sa.dims_for(2, 8, 3, 4, 2, 2, 1)) == 1
         assert call(dims=sa.dims_for(2, 8, 2, 4, 2, 2, 513)) == 2
         assert call(dims=sa.dims_for(2, 8, 2, 4, 2, 2, 1, head_dim=64)) == 2
+        assert call(dims=sa.dims_for(2, 8, 2, 4, 2, (1 << 30) + 1, 1)) == 2
         for bad in (dict(q=None), dict(qo=None), dict(qs=1000), dict(k=None), dict(k=PTR + 4), dict(ks=260), dict(v=None),
                     dict(vs=128), dict(qo=PTR + 8), dict(bt=None), dict(sl=None), dict(ql=None)):
             assert call(**bad) == 1, bad

@@ -242,6 +242,57 @@ def test_select_in_place_on_one_workspace_and_in_a_graph():
             assert np.array_equal(got.cpu().numpy(), w)
 
 
+def test_two_graphs_on_one_workspace():
+    cases = [draws(41, 3, 4, 30000), draws(42, 7, 2, 9000, torch.bfloat16)]
+    ws = torch.zeros(max(sa.beam_select_workspace_size(*x.shape, 4) for x, _, _ in cases), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for x, s, _ in cases:
+        B = x.shape[0]
+        st = (x.cuda(), dev_tensor(s.astype(np.float32)), *(torch.zeros(B, 4, dtype=torch.int32, device="cuda") for _ in range(2)),
+              torch.zeros(B, 4, device="cuda"), ws)
+        sa.beam_select(*st)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sa.beam_select(*st)
+        graphs.append((graph, st, run_select(x, s, 4)))
+    for _ in range(3):
+        for graph, st, _ in graphs:
+            st[2].fill_(-1)
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, st, want in graphs:
+        for got, e in zip(st[2:5], want):
+            assert np.array_equal(got.cpu().numpy(), e)
+
+
+def test_end_tokens_are_flagged_without_finished_beams():
+    x, s, _ = draws(43, 4, 3, 500)
+    x[:, 1, 77] = 60.0
+    s[:, 1] = -0.5
+    tok, par = (torch.zeros(4, 3, dtype=torch.int32, device="cuda") for _ in range(2))
+    fo, sc = torch.full((4, 3), -1, dtype=torch.int32, device="cuda"), torch.zeros(4, 3, device="cuda")
+    ws = torch.zeros(sa.beam_select_workspace_size(4, 3, 500, 3), dtype=torch.uint8, device="cuda")
+    sa.beam_select(x.cuda(), dev_tensor(s.astype(np.float32)), tok, par, sc, ws, finished_out=fo, eos_token=77)
+    assert torch.equal(fo, (tok == 77).int()) and (tok[:, 0] == 77).all()
+
+
+def test_select_binding_refuses():
+    x, s = torch.zeros(2, 3, 40, device="cuda"), torch.zeros(2, 3, device="cuda")
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(sa.beam_select_workspace_size(2, 3, 40, 3), dtype=torch.uint8, device="cuda")
+    good = dict(logits=x, scores=s, tokens=i32(2, 3), parents=i32(2, 3), scores_out=torch.zeros(2, 3, device="cuda"), workspace=ws)
+    sa.beam_select(**good)
+    for change in (dict(logits=x.double()), dict(logits=x[0]), dict(logits=x.transpose(1, 2)), dict(logits=x[:, ::2]), dict(scores=s[:1]),
+                   dict(scores=s.int()), dict(tokens=i32(2, 3).long()), dict(parents=i32(3, 2)), dict(scores_out=i32(2, 3)),
+                   dict(workspace=ws.cpu()), dict(finished=i32(2, 2), eos_token=1), dict(finished_out=i32(2, 3).cpu(), eos_token=1)):
+        with pytest.raises(ValueError):
+            sa.beam_select(**{**good, **change})
+    for change in (dict(logits=x[:1, :1].expand(2, 3, 40)), dict(finished=i32(2, 3)), dict(finished=i32(2, 3), eos_token=40),
+                   dict(workspace=ws[256:])):
+        with pytest.raises((sa.SpecAttnError, ValueError)):
+            sa.beam_select(**{**good, **change})
+
+
 def test_select_on_two_streams_at_once():
     cases = [draws(31 + i, 8, 4, 60000) for i in range(2)]
     want = [run_select(x, s, 4) for x, s, _ in cases]
