@@ -967,7 +967,7 @@ static int reorder_impl(const sa_dims *dims, int32_t beam_width, const int32_t *
     const sa_dims &d = *dims;
     if (beam_width <= 0 || d.num_seqs % beam_width != 0) return SA_ERR_ARG;
     if (beam_width > kMaxBeamWidth) return SA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(d.num_seqs) * d.num_kv_heads > INT32_MAX) return SA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d.num_seqs) * d.num_kv_heads > INT32_MAX / 2) return SA_ERR_UNSUPPORTED;
     if (d.num_seqs == 0) return SA_OK;
     if (!parents || !seq_lens || !k_pool || !v_pool || (bits != 16 && (!k_scales || !v_scales))) return SA_ERR_ARG;
     if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scales, 4) || !aligned(v_scales, 4))

@@ -22,7 +22,11 @@
 // `parts`-th four rows of one; the loads go through a ring in shared memory
 // (asynchronous copies, each lane its own bytes, so no barrier), three steps
 // ahead. Bound: bytes moved (a row in, a row out) for many tokens, two
-// dependent memory round trips (lengths, then rows) for few.
+// dependent memory round trips (lengths, then rows) for few. Measured (device
+// time, 32 query and 8 KV heads): 4096 tokens, dense 15.4 us (5.4 TB/s; an
+// elementwise kernel on as many bytes takes 14.1), into bf16 pages 20.4 us (4.9
+// TB/s), into int8 pages 24.3 us, where the quantising arithmetic counts; one
+// token 2.2 us, 64 tokens into pages 3.3 us.
 #include <cfloat>
 
 #include "common.cuh"
