@@ -18,15 +18,15 @@
 // With the angles and the weights the row's values A, B of the pairs become
 // r (A wc - B ws), r (A ws' + B wc'); the four products are made once a token and
 // kept in shared memory. A warp turns four rows at a time, in packed 32-bit
-// arithmetic, about a hundred instructions. It takes one token, or every
+// arithmetic, about 200 instructions. It takes one token, or every
 // `parts`-th four rows of one; the loads go through a ring in shared memory
 // (asynchronous copies, each lane its own bytes, so no barrier), three steps
 // ahead. Bound: bytes moved (a row in, a row out) for many tokens, two
 // dependent memory round trips (lengths, then rows) for few. Measured (device
 // time, 32 query and 8 KV heads): 4096 tokens, dense 15.4 us (5.4 TB/s; an
-// elementwise kernel on as many bytes takes 14.1), into bf16 pages 20.4 us (4.9
-// TB/s), into int8 pages 24.3 us, where the quantising arithmetic counts; one
-// token 2.2 us, 64 tokens into pages 3.3 us.
+// elementwise kernel on as many bytes takes 14.1), into bf16 pages 18.8 us (5.4
+// TB/s), into int8 pages 21.4 us, where the quantising arithmetic counts; one
+// token 2.1 us, 64 tokens into pages 3.0 us.
 #include <cfloat>
 
 #include "common.cuh"
@@ -255,36 +255,30 @@ struct TokenPlace {
     int first;  // the sequence's first packed row
 };
 
-// The sequences that own the packed rows [token, token + kWarps), from all
-// sequences' query counts: each thread sums a run of them, a block-wide scan
-// gives the runs' starts, and the threads whose runs hold the rows walk them.
-// seq is -1 behind the last row. Block 0 also checks every sequence (each block
-// skips the rows of a bad one).
-__device__ __forceinline__ void locate(const RopeParams &P, int token, TokenPlace (&place)[kWarps]) {
-    __shared__ uint32_t s_total[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The sequence that owns a packed row, from all sequences' query counts: each
+// lane sums a run of them, a scan gives the runs' starts, and the lane whose run
+// holds the row walks it. seq is -1 behind the last row. The first warp also
+// checks every sequence (each warp skips the rows of a bad one).
+__device__ __forceinline__ TokenPlace locate(const RopeParams &P, int token, bool check) {
+    const int lane = threadIdx.x & 31;
     // rows are counted up to one past the last
     const uint32_t cap = static_cast<uint32_t>(P.total_q) + 1;
     auto plus = [cap](uint32_t a, uint32_t b) { return min(a + b, cap); };
     auto rows_of = [&](int n) { return min(static_cast<uint32_t>(max(n, 0)), cap); };
-    const int per = (P.B + kThreads - 1) / kThreads;
-    const int lo = min(P.B, static_cast<int>(threadIdx.x) * per), hi = min(P.B, lo + per);
+    const int per = (P.B + 31) >> 5;
+    const int lo = min(P.B, lane * per), hi = min(P.B, lo + per);
     const int n0 = lo < hi ? P.q_lens[lo] : 0, len0 = lo < hi ? P.seq_lens[lo] : 0;
     uint32_t sum = rows_of(n0);
     for (int b = lo + 1; b < hi; ++b) sum = plus(sum, rows_of(P.q_lens[b]));
-    uint32_t incl = sum;
+    uint32_t next = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl = plus(incl, up);
+        const uint32_t up = __shfl_up_sync(0xffffffffu, next, o);
+        if (lane >= o) next = plus(next, up);
     }
-    uint32_t at = __shfl_up_sync(0xffffffffu, incl, 1);
+    uint32_t at = __shfl_up_sync(0xffffffffu, next, 1);
     if (lane == 0) at = 0;
-    if (lane == 31) s_total[warp] = incl;
-    if (threadIdx.x < kWarps) place[threadIdx.x].seq = -1;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) at = plus(at, s_total[w]);
-    if (blockIdx.x == 0) {
+    if (check) {
         bool bad = false;
         uint32_t a = at;
         for (int b = lo; b < hi; ++b) {
@@ -294,16 +288,22 @@ __device__ __forceinline__ void locate(const RopeParams &P, int token, TokenPlac
         }
         if (bad) flag_error(P.err, kErrBitQlen);
     }
-    const uint32_t first = token, end = first + kWarps;
-    if (at < end && plus(at, sum) > first) {
-        for (int b = lo; b < hi && at < end; ++b) {
-            const uint32_t n = rows_of(b == lo ? n0 : P.q_lens[b]), next = plus(at, n);
-            for (uint32_t row = max(at, first); row < min(next, end); ++row)
-                place[row - first] = TokenPlace{b, static_cast<int>(n), b == lo ? len0 : P.seq_lens[b], static_cast<int>(at)};
-            at = next;
+    const uint32_t row = token;
+    const bool owner = at <= row && row < next;
+    const uint32_t who = __ballot_sync(0xffffffffu, owner);
+    TokenPlace place{lo, n0, len0, static_cast<int>(at)};
+    if (owner) {
+        while (row >= at + rows_of(place.n)) {
+            at += rows_of(place.n);
+            place = TokenPlace{place.seq + 1, P.q_lens[place.seq + 1], P.seq_lens[place.seq + 1], static_cast<int>(at)};
         }
     }
-    __syncthreads();
+    const int from = who != 0 ? __ffs(who) - 1 : 0;
+    place.seq = who != 0 ? __shfl_sync(0xffffffffu, place.seq, from) : -1;
+    place.n = __shfl_sync(0xffffffffu, place.n, from);
+    place.len = __shfl_sync(0xffffffffu, place.len, from);
+    place.first = __shfl_sync(0xffffffffu, place.first, from);
+    return place;
 }
 
 // KB: 0 for dense keys (no pages), 16 for bf16 pages, 8 or 4 for code pages.
@@ -327,16 +327,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     const float freq0 = lane < P.half ? P.inv_freq[lane] : 0.f;
     const float freq1 = lane + 32 < P.half ? P.inv_freq[lane + 32] : 0.f;
 
+    if (token >= P.total_q) return;
     int pos, pid = 0, slot = 0;
     if constexpr (KB == 0) {
-        if (token >= P.total_q) return;
         pos = P.positions[token];
     } else {
-        __shared__ TokenPlace s_place[kWarps];
-        const int token0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * kWarps >> P.parts_log2);
-        locate(P, token0, s_place);
-        if (token >= P.total_q) return;
-        const TokenPlace at = s_place[token - token0];
+        const TokenPlace at = locate(P, token, gw == 0);
         if (at.seq < 0 || at.n > at.len || at.n > P.max_q_len || at.first + static_cast<long long>(at.n) > P.total_q)
             return;
         pos = at.len - at.n + (token - at.first);
