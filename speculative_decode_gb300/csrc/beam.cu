@@ -51,7 +51,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;       // collected candidates of a chunk
 constexpr int kRankMost = 128;   // ranked by counting up to this many
-constexpr int kMergeCap = 1024;  // entries of one merge step
+constexpr int kMergeCap = 1024;  // entries of a merge step where one block's threads are too few
 constexpr int kMaxBatches = 16;  // batches of a chunk
 constexpr int kTops = 4;         // largest lane maxima of a warp
 static_assert(kWarps * kTops == 32 && kMaxBeamWidth <= 32, "a lane for each, enough for every K");
@@ -59,6 +59,7 @@ constexpr int kMaxBeams = kMaxBeamWidth;
 constexpr int kIndexBits = 27;   // tokens in a merge key
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kLastRank = 128;  // of a merge entry beside its beam: the last rank of the step
 
 // Unsigned integers in the order of the floats (-inf lowest, no NaN).
 __device__ __forceinline__ uint32_t order32(float x) {
@@ -378,13 +379,15 @@ __device__ void fill_rest(SelectShared &S, const SelectParams &P, int g, int n) 
 }
 
 // The last CTA of group g: every row's lse, then the K best of all listed
-// candidates.
-template <typename L>
+// candidates. kMine: entries of a step per thread; one where one step takes them
+// all (its shorter code, run once from a cold instruction cache, saves 0.4 us).
+template <typename L, int kMine>
 __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int row0 = g * P.W;
     const unsigned W = P.W, n_chunks = P.n_chunks, K = P.K;
-    // Entries in steps of kMergeCap, the best of the steps before kept: R ranks
+    constexpr unsigned kStep = kMine * kThreads;
+    // Entries in steps of kStep, the best of the steps before kept: R ranks
     // of all lists, then the next R, until no list's last one may still matter.
     // They are the lists' in turn, consecutive lists of different rows, shifted from
     // chunk to chunk; entry 8 q + r of a step goes to lane q of warp (q + r) % 8. So
@@ -405,7 +408,6 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
     auto key_of = [&](unsigned w, unsigned chunk, unsigned rank) {
         return rank < K ? __ldcg(P.part_keys + (static_cast<int64_t>(row0 + w) * n_chunks + chunk) * K + rank) : 0;
     };
-    constexpr int kMine = kMergeCap / kThreads;
     uint64_t mine[kMine];
 #pragma unroll
     for (int u = 0; u < kMine; ++u) {
@@ -512,17 +514,16 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
 #pragma unroll
         for (int u = 0; u < kMine; ++u)
             if (mine[u] != 0 && !(most[u] < floor)) {
-                if (last_rank[u]) S.more = 1;
                 const int at = atomicAdd(&S.n, 1);
                 if (at < kRankMost) {
                     S.keys[at] = mine[u];
-                    S.beam_of[at] = static_cast<uint8_t>(of[u]);
+                    S.beam_of[at] = static_cast<uint8_t>(of[u] | (last_rank[u] ? kLastRank : 0));
                 }
             }
         __syncthreads();
         const int got = S.n;
         if (got <= kRankMost) {
-            if (t >= n && t < got) S.kept[t] = candidate(S.keys[t], S.beam_of[t]);
+            if (t >= n && t < got) S.kept[t] = candidate(S.keys[t], S.beam_of[t] & (kLastRank - 1));
             __syncthreads();
             for (int c = lane; c < got; c += 32) {
                 const Candidate mine_c = S.kept[c];
@@ -531,13 +532,19 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
                 if (ahead != 0) atomicAdd(&S.rank[c], ahead);
             }
             __syncthreads();
-            if (t < got && S.rank[t] < static_cast<int>(K)) S.best[S.rank[t]] = S.kept[t];
+            if (t < got && S.rank[t] < static_cast<int>(K)) {
+                S.best[S.rank[t]] = S.kept[t];
+                if (t >= n && S.beam_of[t] >= kLastRank) S.more = 1;  // its list may give more
+            }
             n = min(got, static_cast<int>(K));
         } else {  // one by one
             Candidate all[kMine + 1];
 #pragma unroll
             for (int u = 0; u < kMine; ++u) all[u] = mine[u] != 0 ? candidate(mine[u], of[u]) : Candidate{0, 0};
             all[kMine] = t < n ? S.kept[t] : Candidate{0, 0};
+#pragma unroll
+            for (int u = 0; u < kMine; ++u)
+                if (last_rank[u] && mine[u] != 0 && !(most[u] < floor)) S.more = 1;
             Candidate last{~0ull, ~0ull};
             for (int k = 0; k < static_cast<int>(K); ++k) {
                 Candidate c{0, 0};
@@ -560,7 +567,7 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
             n = static_cast<int>(K);  // more than K entries have a value
         }
         __syncthreads();
-        e0 += kMergeCap;
+        e0 += kStep;
         if (e0 >= lists * R) {  // these ranks are done
             if (S.more == 0) break;
             __syncthreads();
@@ -828,7 +835,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
     }
     __syncthreads();
     if (!S.last) return;
-    merge_group<L>(S, P, g);
+    if (P.W * P.n_chunks * P.K <= kThreads) merge_group<L, 1>(S, P, g);
+    else merge_group<L, kMergeCap / kThreads>(S, P, g);
     if (t == 0) P.counters[g] = 0;
 }
 
@@ -880,8 +888,10 @@ __global__ void __launch_bounds__(kThreads, kReorderCtas) beam_reorder_kernel(co
     const int64_t a = (static_cast<int64_t>(src) * P.Hkv + head) * kPageSize;
     const int64_t b = (static_cast<int64_t>(dst) * P.Hkv + head) * kPageSize;
     const int vecs = rem * (P.row_bytes / 16);
-    const uint4 *s = reinterpret_cast<const uint4 *>(P.pools[pool] + a * P.row_bytes);
-    uint4 *d = reinterpret_cast<uint4 *>(P.pools[pool] + b * P.row_bytes);
+    char *rows = pool == 0 ? P.pools[0] : P.pools[1];
+    float *scales = pool == 0 ? P.scales[0] : P.scales[1];
+    const uint4 *s = reinterpret_cast<const uint4 *>(rows + a * P.row_bytes);
+    uint4 *d = reinterpret_cast<uint4 *>(rows + b * P.row_bytes);
     for (int v0 = threadIdx.x; v0 < vecs; v0 += kReorderFlight * kThreads) {
         uint4 r[kReorderFlight];
 #pragma unroll
@@ -891,8 +901,8 @@ __global__ void __launch_bounds__(kThreads, kReorderCtas) beam_reorder_kernel(co
         for (int u = 0; u < kReorderFlight; ++u)
             if (v0 + u * kThreads < vecs) d[v0 + u * kThreads] = r[u];
     }
-    if (P.scales[pool] != nullptr)
-        for (int k = threadIdx.x; k < rem; k += kThreads) P.scales[pool][b + k] = P.scales[pool][a + k];
+    if (scales != nullptr)
+        for (int k = threadIdx.x; k < rem; k += kThreads) scales[b + k] = scales[a + k];
 }
 
 }  // namespace
