@@ -13,9 +13,9 @@
 // Each thread carries its maximum and its sum of exp(x - max), and keeps every
 // batch's maximum in shared memory. The K largest logits are found afterwards (a
 // row's order is its logits' order, so no sum is needed to choose them): each
-// of the eight warps gives its four largest lane maxima; the K-th largest of
-// these 32 is reached by K lanes, so by the K largest logits of the chunk, and
-// by few others. The batches whose maximum reaches it are read again, from the L2,
+// of the eight warps gives its four largest lane maxima (eight for K above 16);
+// the K-th largest of these is reached by K lanes, so by the K largest logits of
+// the chunk, and by few others. The batches whose maximum reaches it are read again, from the L2,
 // and their values that reach it ranked by counting. When many do (heavy ties) the
 // lowest tokens among the equal ones are taken in order, and otherwise the
 // values one by one as block-wide maxima.
@@ -50,11 +50,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;       // collected candidates of a chunk
-constexpr int kRankMost = 128;   // ranked by counting up to this many
+constexpr int kRankMost = 256;   // ranked by counting up to this many, a thread for each
 constexpr int kMergeCap = 1024;  // entries of a merge step where one block's threads are too few
 constexpr int kMaxBatches = 16;  // batches of a chunk
-constexpr int kTops = 4;         // largest lane maxima of a warp
-static_assert(kWarps * kTops == 32 && kMaxBeamWidth <= 32, "a lane for each, enough for every K");
+constexpr int kTops = 8;         // largest lane maxima of a warp, four of them for K up to 16
+static_assert(kRankMost == kThreads && kWarps * kTops == 64 && kMaxBeamWidth <= 32, "a lane for two of them");
 constexpr int kMaxBeams = kMaxBeamWidth;
 constexpr int kIndexBits = 27;   // tokens in a merge key
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
@@ -302,32 +302,52 @@ __device__ __forceinline__ double log_of_sum(float hi, float lo) {
     return static_cast<double>(k) * 0.69314718055994530942 + (static_cast<double>(2.f * z) + static_cast<double>(small));
 }
 
-// The warp's kTops largest of the lanes' keys to S.top (0 where fewer lanes have one).
-__device__ __forceinline__ void put_tops(SelectShared &S, uint32_t key) {
+// The warp's kCount largest lanes' keys to S.top (0 where fewer lanes have one).
+template <int kCount>
+__device__ __forceinline__ void put_tops_of(SelectShared &S, uint32_t key) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < kTops; ++j) {
+    for (int j = 0; j < kCount; ++j) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, key);
         const uint32_t who = __ballot_sync(0xffffffffu, key == top);
         if (lane == j) mine = top;
         if (lane == __ffs(who) - 1) key = 0;
     }
-    if (lane < kTops) S.top[warp * kTops + lane] = mine;
+    if (lane < kCount) S.top[warp * kCount + lane] = mine;
 }
 
-// The K-th largest of S.top, one a lane: at least K lanes of the block have a
-// key that reaches it.
+// Four, and eight for K above 16, where the 32nd of 32 would let too many pass.
+__device__ __forceinline__ void put_tops(SelectShared &S, uint32_t key, int K) {
+    if (K <= 16) put_tops_of<kTops / 2>(S, key);
+    else put_tops_of<kTops>(S, key);
+}
+
+// How many of S.top's first kCount come before the one at `at`.
+template <int kCount>
+__device__ __forceinline__ int tops_before(const SelectShared &S, int at) {
+    const uint32_t mine = S.top[at];
+    int ahead = 0;
+#pragma unroll(kCount == 32 ? 32 : 8)
+    for (int o = 0; o < kCount; ++o) {
+        const uint32_t other = S.top[o];
+        ahead += other > mine || (other == mine && o < at);
+    }
+    return ahead;
+}
+
+// The K-th largest of them: at least K lanes of the block have a key that reaches it.
 __device__ __forceinline__ uint32_t kth_top(const SelectShared &S, int K) {
     const int lane = threadIdx.x & 31;
-    const uint32_t mine = S.top[lane];
-    int ahead = 0;
-#pragma unroll
-    for (int o = 0; o < 32; ++o) {
-        const uint32_t other = S.top[o];
-        ahead += other > mine || (other == mine && o < lane);
+    uint32_t who;
+    if (K <= 16) {
+        who = __ballot_sync(0xffffffffu, tops_before<32>(S, lane) == K - 1);
+        return S.top[__ffs(who) - 1];
     }
-    return __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, ahead == K - 1)) - 1);
+    who = __ballot_sync(0xffffffffu, tops_before<64>(S, lane) == K - 1);
+    if (who != 0) return S.top[__ffs(who) - 1];
+    who = __ballot_sync(0xffffffffu, tops_before<64>(S, lane + 32) == K - 1);
+    return S.top[32 + __ffs(who) - 1];
 }
 
 // The slots behind the `n` continuations of a value above -inf: continuations
@@ -504,7 +524,7 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
             const float low = value - err;
             if (low > -INFINITY) least = max(least, order32(low));
         }
-        put_tops(S, least);
+        put_tops(S, least, K);
         if (t == 0) S.n = n;
         if (t < kRankMost) S.rank[t] = 0;
         if (t < n) S.kept[t] = S.best[t];
@@ -808,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
         float warp_sum = m > -INFINITY ? sum * ex2((m - warp_m) * kLog2e) : 0.f;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) warp_sum += __shfl_xor_sync(0xffffffffu, warp_sum, o);
-        put_tops(S, key);
+        put_tops(S, key, P.K);
         if (lane == 0) {
             S.m[warp] = warp_m;
             S.s[warp] = warp_sum;
