@@ -470,7 +470,9 @@ SA_API int sa_qk_norm_rope(const sa_rope *rope, int32_t num_tokens, int32_t num_
  * Rows of q_out behind the last sequence's are not written. A sequence whose
  * q_lens or seq_lens are inconsistent sets SA_ERR_QLEN and is skipped; a page id
  * out of range sets SA_ERR_PAGE_OOB and the page rows are skipped.
- * Like sa_kv_append the kernel lets a following sa_paged_attn start early.
+ * Like sa_kv_append the kernel lets a following sa_paged_attn start early. (This
+ * kernel and those of the calls below are themselves launched while the kernel
+ * before them on the stream ends, and wait for it before they read anything.)
  *
  * sa_kv_append_rope_q8, sa_kv_append_rope_q4: the same into int8 and int4 pages
  * (formats of sa_kv_append_q8 and _q4, 16-byte aligned codes); keys are

@@ -775,6 +775,7 @@ template <typename L, bool kAligned>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectParams P) {
     using C = Chunk<L, kAligned>;
     __shared__ SelectShared S;
+    grid_dependency_wait();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const unsigned row = blockIdx.x / static_cast<unsigned>(P.n_chunks);
     const int chunk_at = static_cast<int>(blockIdx.x - row * P.n_chunks);
@@ -866,6 +867,7 @@ constexpr int kReorderFlight = 8;  // 16-byte loads in flight per thread
 
 // One CTA per (child, KV head, pool).
 __global__ void __launch_bounds__(kThreads, kReorderCtas) beam_reorder_kernel(const ReorderParams P) {
+    grid_dependency_wait();
     const unsigned unit = blockIdx.x >> 1, child = unit / static_cast<unsigned>(P.Hkv);
     const int pool = blockIdx.x & 1, head = static_cast<int>(unit - child * P.Hkv);
     const int lane = threadIdx.x & 31;
@@ -942,13 +944,11 @@ cudaError_t launch_beam_select(SelectParams p, bool bf16, bool aligned, cudaStre
     const int64_t ctas = static_cast<int64_t>(p.B) * p.W * p.n_chunks;
     auto kernel = bf16 ? (aligned ? beam_select_kernel<Logits16, true> : beam_select_kernel<Logits16, false>)
                        : (aligned ? beam_select_kernel<Logits32, true> : beam_select_kernel<Logits32, false>);
-    kernel<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, static_cast<unsigned>(ctas), kThreads, p, stream);
 }
 
 cudaError_t launch_beam_reorder(const ReorderParams &p, cudaStream_t stream) {
-    beam_reorder_kernel<<<2u * static_cast<unsigned>(p.num_seqs) * p.Hkv, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(beam_reorder_kernel, 2u * static_cast<unsigned>(p.num_seqs) * p.Hkv, kThreads, p, stream);
 }
 
 }  // namespace sa

@@ -169,6 +169,24 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes
 // kernel was not launched as a dependent).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Launch a kernel as a programmatic dependent of the one before it on the
+// stream: its launch overlaps that kernel's end. The kernel starts with
+// grid_dependency_wait().
+template <typename Params>
+cudaError_t launch_dependent(void (*kernel)(Params), unsigned grid, unsigned threads, const Params &params,
+                             cudaStream_t stream) {
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.stream = stream;
+    cudaLaunchAttribute attribute[1];
+    attribute[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attribute[0].val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = attribute;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, params);
+}
+
 // Two floats -> packed bf16x2 (lo in bits 0..15), round to nearest even.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t d;

@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     // a lane's products: 8 pairs of A wc, -B ws, A ws, B wc as two runs of four
     __shared__ __align__(16) float s_mul[kWarps][4][kHeadDim / 2];
     __shared__ float s_cos[kWarps][kHeadDim / 2], s_sin[kWarps][kHeadDim / 2];
+    grid_dependency_wait();
     // the attention kernel that follows reads q and the pages only after this
     // grid has completed
     if constexpr (KB != 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -492,8 +493,7 @@ cudaError_t launch_rope(RopeParams p, int code_bits, int sms, cudaStream_t strea
     }
     const int64_t warps = static_cast<int64_t>(p.total_q) << p.parts_log2;
     auto kernel = p.interleaved ? kernel_for<true>(code_bits) : kernel_for<false>(code_bits);
-    kernel<<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, static_cast<unsigned>((warps + kWarps - 1) / kWarps), kThreads, p, stream);
 }
 
 }  // namespace sa
