@@ -518,7 +518,7 @@ __device__ void merge_group(SelectShared &S, const SelectParams &P, int g) {
             if (!S.done[w]) {
                 const float x = order32_value(static_cast<uint32_t>(mine[u] >> 32)), lse = static_cast<float>(S.lse[w]);
                 value = score + (x - lse);
-                err = (fabsf(x) + fabsf(lse) + fabsf(score)) * 0x1p-22f;
+                err = (fabsf(x) + fabsf(lse) + fabsf(score)) * 0x1p-21f;  // four roundings are 2^-22
             }
             most[u] = value + err;
             const float low = value - err;

@@ -90,6 +90,22 @@ def test_select_of_rows_at_any_address(dtype, offset, pad):
     check_select(x, s, 8, offset=offset, pad=pad)
 
 
+@pytest.mark.parametrize("V", [1000])
+def test_select_of_rows_past_32_bits(V):
+    """Rows whose offsets pass 2^31 values."""
+    x, s, _ = draws(77, 40, 32, V, torch.bfloat16)
+    buf = torch.empty(40, 32, 2_000_000, dtype=torch.bfloat16, device="cuda")
+    view = buf[..., 3:3 + V]
+    view.copy_(x)
+    tok, par = (torch.zeros(40, 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    sc = torch.zeros(40, 4, device="cuda")
+    ws = torch.zeros(sa.beam_select_workspace_size(40, 32, V, 4), dtype=torch.uint8, device="cuda")
+    sa.beam_select(view, dev_tensor(s.astype(np.float32)), tok, par, sc, ws)
+    for g in (0, 20, 39):
+        t, p, _ = ref.beam_select(x[g].float().numpy(), s[g].astype(np.float32), 4)
+        assert np.array_equal(tok[g].cpu().numpy(), t) and np.array_equal(par[g].cpu().numpy(), p)
+
+
 @pytest.mark.parametrize("V", [1, 5, 3000, 128256])
 def test_select_with_finished_beams(V):
     for seed, K in ((0, 6), (1, 3), (2, 12)):
@@ -178,7 +194,8 @@ def test_select_of_the_largest_sizes(B, W, V, K, dtype):
         x.scatter_reduce_(2, spots, torch.rand(B, W, 40, generator=gen, device="cuda") * 16 + 20, "amax")
     x = x.to(dtype)
     s = -torch.rand(B, W, generator=gen, device="cuda")
-    best, tokens = x.double().topk(K, -1)
+    best, tokens = x.float().topk(K, -1)
+    best = best.double()
     parts = max(1, V >> 12)                       # torch sums one long row slowly
     lse = torch.stack([row.view(parts, -1).double().logsumexp(-1).logsumexp(0) for row in x.flatten(0, 1)]).view(B, W, 1) \
         if V > 64 else x.double().logsumexp(-1, keepdim=True)
@@ -357,6 +374,21 @@ def test_reorder(kind, groups, W, T, hkv):
             for a, b, rows in copies:
                 want[b, :, :rows] = p[a, :, :rows]
             assert np.array_equal(g, want)
+
+
+def test_reorder_of_pages_past_32_bits():
+    pages, T = 70000, 300                            # 2.3e9 values a pool
+    kp, vp = (torch.zeros(pages, 1, 256, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kp[69998], vp[69998] = 3.0, 5.0
+    table = torch.tensor([[7, 69998, 1], [7, 69999, 2]], dtype=torch.int32, device="cuda")
+    d = sa.dims_for(2, 4, 1, pages, 3, 2, 1)
+    out = torch.zeros_like(table)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sa.beam_reorder(d, 2, torch.zeros(2, dtype=torch.int32, device="cuda"), table, torch.full((2,), T, dtype=torch.int32, device="cuda"),
+                    out, kp, vp, err_flag=err)
+    assert int(err.item()) == 0 and torch.equal(out, table)
+    for p, value in ((kp, 3.0), (vp, 5.0)):
+        assert (p[69999, 0, :T - 256] == value).all() and (p[69999, 0, T - 256:] == 0).all()
 
 
 def test_reorder_flags_bad_groups_and_pages():

@@ -310,6 +310,33 @@ def test_page_out_of_range_is_flagged_and_skipped():
         assert all(torch.equal(g[page], p[page]) for g, p in zip(got, pool))
 
 
+def test_pages_past_32_bits():
+    rng = np.random.default_rng(71)
+    rope, want = make_rope(rng)
+    pages = 70000                                    # 2.3e9 values a pool
+    kp, vp = (torch.zeros(pages, 1, 256, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.tensor([[4, 69999]], dtype=torch.int32, device="cuda")
+    d = sa.dims_for(1, 2, 1, pages, 2, 3, 3)
+    qkv = bf16(rng, 3, 4, 128).cuda()
+    i32 = lambda n: torch.tensor([n], dtype=torch.int32, device="cuda")  # noqa: E731
+    sa.kv_append_rope(d, rope, None, qkv[:, 2:3], qkv[:, 3:], None, kp, vp, table, i32(300), i32(3))
+    assert_rows(kp[69999, 0, 41:44], *(a[:, 0] for a in want(qkv[:, 2:3].float().cpu().numpy(), np.arange(297, 300), 1)))
+    assert torch.equal(vp[69999, 0, 41:44], qkv[:, 3]) and (kp[69999, 0, 44:] == 0).all() and (kp[4] == 0).all()
+
+
+def test_many_tokens_of_many_sequences():
+    """More sequences than lanes search at once, and rows for every warp."""
+    rng = np.random.default_rng(72)
+    q_lens = rng.integers(0, 4, 700)
+    q_lens[0] = 1
+    rng, c = append_case(72, q_lens + rng.integers(1, 40, 700), q_lens, hq=3, hkv=1)
+    rope, want = make_rope(rng, rotary=32)
+    pool = pools(rng, "bf16", c["pages"], 1)
+    q_out, got, err = call_append("bf16", rope, c, pool)
+    assert err == 0
+    check_append("bf16", c, want, q_out, got, pool)
+
+
 def test_binding_refuses_wrong_tensors():
     rng, c = append_case(65, [30, 20], [2, 4])
     rope, _ = make_rope(rng)
