@@ -199,8 +199,8 @@ struct Chunk {
         }
         return p;
     }
-    // The values of a piece, tamed.
-    __device__ __forceinline__ void values(const Piece<kAligned> &p, float (&x)[kVec]) const {
+    // The values of a piece in pairs, as they are.
+    __device__ __forceinline__ void pairs(const Piece<kAligned> &p, uint64_t *x) const {
         uint4 v = p.a;
         if constexpr (!kAligned) {
             if (!p.end) {
@@ -214,15 +214,22 @@ struct Chunk {
                 }
             }
         }
-        x[0] = tamed(L::template value<0>(v));
-        x[1] = tamed(L::template value<1>(v));
-        x[2] = tamed(L::template value<2>(v));
-        x[3] = tamed(L::template value<3>(v));
+        x[0] = two(L::template value<0>(v), L::template value<1>(v));
+        x[1] = two(L::template value<2>(v), L::template value<3>(v));
         if constexpr (kVec == 8) {
-            x[4] = tamed(L::template value<4>(v));
-            x[5] = tamed(L::template value<5>(v));
-            x[6] = tamed(L::template value<6>(v));
-            x[7] = tamed(L::template value<7>(v));
+            x[2] = two(L::template value<4>(v), L::template value<5>(v));
+            x[3] = two(L::template value<6>(v), L::template value<7>(v));
+        }
+    }
+    // The values of a piece, tamed.
+    __device__ __forceinline__ void values(const Piece<kAligned> &p, float (&x)[kVec]) const {
+        uint64_t two_of[kVec / 2];
+        pairs(p, two_of);
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {
+            const float2 v = apart(two_of[e]);
+            x[2 * e] = tamed(v.x);
+            x[2 * e + 1] = tamed(v.y);
         }
     }
     template <int Q>
@@ -803,24 +810,41 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectPa
             constexpr int kPart = C::kLoads < 16 / C::kVec ? C::kLoads : 16 / C::kVec;  // pieces at once
 #pragma unroll
             for (int i0 = 0; i0 < C::kLoads; i0 += kPart) {
-                float x[kPart][C::kVec];
-                float part_top = -INFINITY;
+                constexpr int kPairs = kPart * C::kVec / 2;
+                uint64_t x[kPairs];
 #pragma unroll
-                for (int i = 0; i < kPart; ++i) {
-                    chunk.values(now[i0 + i], x[i]);
+                for (int i = 0; i < kPart; ++i) chunk.pairs(now[i0 + i], x + i * C::kVec / 2);
+                // The values are taken as they are; where NaN or +inf are among them,
+                // which the sum shows, they are tamed and taken again.
+                float part_top, part_sum, base;
+                for (;;) {
+                    part_top = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < C::kVec; ++e) part_top = fmaxf(part_top, x[i][e]);
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float2 v = apart(x[e]);
+                        part_top = fmaxf(part_top, fmaxf(v.x, v.y));
+                    }
+                    const float m_new = fmaxf(m, part_top);
+                    base = m_new > -INFINITY ? m_new : 0.f;
+                    const uint64_t minus = two(-base, -base), scale = two(kLog2e, kLog2e);
+                    uint64_t sums[2] = {0, 0};
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float2 v = apart(mul2(add2(x[e], minus), scale));
+                        sums[e & 1] = add2(sums[e & 1], two(ex2(v.x), ex2(v.y)));
+                    }
+                    const float2 both = apart(add2(sums[0], sums[1]));
+                    part_sum = both.x + both.y;
+                    if (part_sum <= FLT_MAX) break;
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float2 v = apart(x[e]);
+                        x[e] = two(tamed(v.x), tamed(v.y));
+                    }
                 }
                 top = fmaxf(top, part_top);
-                const float m_new = fmaxf(m, part_top);
-                const float base = m_new > -INFINITY ? m_new : 0.f;
-                float part[4] = {sum * ex2((m - base) * kLog2e), 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < kPart; ++i)
-#pragma unroll
-                    for (int e = 0; e < C::kVec; ++e) part[e & 3] += ex2((x[i][e] - base) * kLog2e);
-                sum = (part[0] + part[1]) + (part[2] + part[3]);
-                m = m_new;
+                sum = fmaf(sum, ex2((m - base) * kLog2e), part_sum);
+                m = fmaxf(m, part_top);
             }
             S.batch_max[b][t] = top;
         }
