@@ -23,10 +23,10 @@
 // (asynchronous copies, each lane its own bytes, so no barrier), three steps
 // ahead. Bound: bytes moved (a row in, a row out) for many tokens, two
 // dependent memory round trips (lengths, then rows) for few. Measured (device
-// time, 32 query and 8 KV heads): 4096 tokens, dense 15.4 us (5.4 TB/s; an
-// elementwise kernel on as many bytes takes 14.1), into bf16 pages 18.8 us (5.4
-// TB/s), into int8 pages 21.4 us, where the quantising arithmetic counts; one
-// token 2.1 us, 64 tokens into pages 3.0 us.
+// time, 32 query and 8 KV heads): 4096 tokens, dense 15.2 us (5.5 TB/s; an
+// elementwise kernel on as many bytes takes 14.1), into bf16 pages 18.9 us (5.3
+// TB/s), into int8 pages 23.1 us, where the quantising arithmetic counts; one
+// token 1.9 us, 64 tokens into pages 3.0 us.
 #include <cfloat>
 
 #include "common.cuh"
