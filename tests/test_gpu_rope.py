@@ -249,6 +249,52 @@ def test_append_without_queries_at_given_positions():
     check_append("bf16", c, want, None, got, pool, positions=positions, with_q=False)
 
 
+@pytest.mark.parametrize("kind", ["q8", "q4"])
+def test_codes_at_borders_and_of_extreme_rows(kind):
+    """Codes and scales are those of IEEE divisions, as kv_append takes them: rows
+    of every power of two down to subnormal ones, values on the border of two
+    codes (few bits, so many), rows of zeros, with infinities and NaN."""
+    rng = np.random.default_rng(65)
+    n, hkv, top = 510, 4, 127 if kind == "q8" else 7
+    rows = n * hkv
+    x = rng.uniform(-1, 1, (rows, 128)).astype(np.float32)
+    x[1::4] = (rng.integers(-top, top + 1, (len(x[1::4]), 128)) + 0.5 * rng.integers(0, 2, (len(x[1::4]), 128))) / top
+    x[1::4, 7] = 1.0
+    x = np.ldexp(np.clip(x, -1, 1), rng.integers(-139, 128, (rows, 1))).astype(np.float32)
+    x[5] = 0.0
+    x[6, 1:] = 0.0
+    x[7, 3], x[8, 127], x[9, 0], x[9, 64] = np.inf, -np.inf, np.nan, np.inf
+    x[10, ::2], x[11] = np.nan, np.nan
+    x[12, 100] = np.nan
+    bits = torch.from_numpy(x).to(torch.bfloat16).reshape(n, hkv, 128).cuda()
+    pages = -(-n // 256)
+    d = sa.dims_for(1, hkv, hkv, pages, pages, n, n)
+    shape = (pages, hkv, 256)
+    width = 128 if kind == "q8" else 64
+    ints = [dev_tensor(np.array(a, np.int32)) for a in ([list(range(pages))], [n], [n])]
+    results = []
+    for fused in (True, False):
+        codes = [torch.zeros(*shape, width, dtype=torch.int8 if kind == "q8" else torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(*shape, dtype=torch.float32, device="cuda") for _ in range(2)]
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        if fused:
+            fn = sa.kv_append_rope_q8 if kind == "q8" else sa.kv_append_rope_q4
+            fn(d, sa.Rope(rotary_dim=0), None, bits, bits, None, *codes, *scales, *ints, err_flag=err)
+        else:
+            fn = sa.kv_append_q8 if kind == "q8" else sa.kv_append_q4
+            fn(d, bits, bits, *codes, *scales, *ints, err_flag=err)
+        assert int(err.item()) == 0
+        results.append([t.cpu().numpy() for t in codes + scales])
+    for got, want in zip(*results):
+        assert np.array_equal(got, want, equal_nan=got.dtype == np.float32)
+    finite = np.isfinite(x).all(-1) & (np.abs(bits.float().cpu().numpy().reshape(rows, 128)) < np.inf).all(-1)
+    quant = oracle.quantize_q8 if kind == "q8" else oracle.quantize_q4
+    want, scale = quant(bits.cpu().view(torch.int16).numpy().view(np.uint16).reshape(rows, 128)[finite])
+    code, step = (a.transpose(0, 2, 1, *range(3, a.ndim)).reshape(pages * 256, hkv, -1)[:n].reshape(rows, -1)
+                  for a in (results[0][0], results[0][2]))
+    assert np.array_equal(code[finite], want) and np.array_equal(step[finite, 0], scale)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "q8", "q4"])
 def test_no_norm_and_no_rotation_is_kv_append(kind):
     rng, c = append_case(61, [300, 20, 513], [5, 20, 1])
